@@ -4,7 +4,9 @@ Argument marshalling only: every step of the projection runs in the library's
 HIP kernels.  PyTorch provides device memory and streams; output tensors are
 allocated here with ``torch.empty`` when the caller passes none.  The names and
 arguments mirror the C ABI in ``include/q8.h``; see there for layouts,
-numerics and errors.
+numerics and errors.  The steps of a decode step around the projections (the
+mixture-of-experts layer, the sampler; ``include/q8_decode.h``) are in
+``decode.py`` and re-exported here.
 
 The library must be built (``python q8_projection_amd/build.py``); importing
 this module without it, or calling a projection without a GPU, raises.
@@ -44,6 +46,11 @@ SIGNATURES = {
     "q8_block_sums": (_I, [_I, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
     "q8_status_name": (ctypes.c_char_p, [_I]),
     "q8_version": (_I, []),
+    # include/q8_decode.h
+    "q8_moe_workspace_bytes": (_I64, [_P, _I64]),
+    "q8_moe_route": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _P]),
+    "q8_moe_experts": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "q8_moe": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
 }
 
 _lib = None
@@ -314,3 +321,6 @@ def block_sums(mode, w: torch.Tensor, n: int, k: int, hi, lo=None, out=None, row
     _check("q8_block_sums", lib().q8_block_sums(m, _ptr(w), n, k, rows, _ptr(hi), _ptr(lo), _ptr(out),
                                                 _stream(stream)))
     return out
+
+
+from .decode import MoeLayer, moe, moe_experts, moe_route, moe_workspace_bytes  # noqa: E402

@@ -1,0 +1,180 @@
+"""Python binding of include/q8_decode.h: the mixture-of-experts layer.
+
+As in the package's other wrappers, argument marshalling only.  Every tensor of
+a call lives on one device, and the call runs on that device whichever is
+current, on ``stream`` or else on that device's current stream.  Outputs and
+workspaces that are not passed are allocated here.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import q8_projection_amd as _q8
+
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
+class _MoeLayerC(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("k", ctypes.c_int64), ("ff", ctypes.c_int64),
+                ("router", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p)]
+
+
+def _need(t, name: str, dtype, shape, device):
+    """Raise ValueError unless t is a contiguous tensor of this dtype, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call(fn: str, device, stream, own, *args):
+    """Call a library function on `device` and `stream` (None: its current
+    stream).  `own`: tensors allocated here, which the caching allocator must
+    not hand out again before the stream is done with them."""
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    elif hasattr(stream, "cuda_stream"):
+        raw = stream.cuda_stream
+        for t in own:
+            if t is not None:
+                t.record_stream(stream)
+    else:
+        raw = int(stream)
+        if own:
+            ext = torch.cuda.ExternalStream(raw, device=device)
+            for t in own:
+                if t is not None:
+                    t.record_stream(ext)
+    f = getattr(_q8.lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, raw)
+    if status != 0:
+        raise _q8.Q8Error(fn, status)
+
+
+class MoeLayer:
+    """A layer's Q8_0 experts and router, checked once.
+
+    w_gate, w_up: uint8 Q8_0 blocks [experts][ff][k/32*34]; w_down [experts][k][ff/32*34];
+    router f32 [experts][k] (None: choices are given to ``moe_experts``).  The tensors
+    are used in place and kept alive by this object.
+    """
+
+    def __init__(self, mode, w_gate, w_up, w_down, k: int, ff: int, top_k: int, router=None,
+                 renormalize: bool = True):
+        if not isinstance(w_gate, torch.Tensor) or w_gate.dim() < 2:
+            raise ValueError("w_gate must be a tensor [experts][ff][k/32*34]")
+        if not w_gate.is_cuda:
+            raise ValueError("w_gate must be a device tensor")
+        self.device = w_gate.device
+        experts = w_gate.shape[0]
+        for name, t, n, cols in (("w_gate", w_gate, ff, k), ("w_up", w_up, ff, k), ("w_down", w_down, k, ff)):
+            _need(t, name, _U8, (experts, n, cols // _q8.BLOCK * _q8.BLOCK_BYTES), self.device)
+        if router is not None:
+            _need(router, "router", _F32, (experts, k), self.device)
+        self.mode = _q8._mode(mode)
+        self.experts, self.top_k, self.k, self.ff = experts, int(top_k), int(k), int(ff)
+        self._tensors = (w_gate, w_up, w_down, router)
+        self._c = _MoeLayerC(self.mode, experts, self.top_k, int(bool(renormalize)), k, ff,
+                             None if router is None else router.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                             w_down.data_ptr())
+        self._ref = ctypes.addressof(self._c)
+        self._bytes = {}
+        if self.workspace_bytes(1) == 0:
+            raise ValueError(f"the library does not take this layer: mode {mode}, {experts} experts, top_k {top_k}, "
+                             f"k {k}, ff {ff}")
+
+    def workspace_bytes(self, rows: int) -> int:
+        """Bytes of the workspace for `rows` rows."""
+        rows = min(int(rows), 64)
+        if rows not in self._bytes:
+            self._bytes[rows] = int(_q8.lib().q8_moe_workspace_bytes(self._ref, rows))
+        return self._bytes[rows]
+
+    def workspace(self, rows: int) -> torch.Tensor:
+        """A zero-filled workspace for calls of up to `rows` rows."""
+        return torch.zeros(self.workspace_bytes(rows), dtype=_U8, device=self.device)
+
+
+def moe_workspace_bytes(layer: MoeLayer, rows: int) -> int:
+    return layer.workspace_bytes(rows)
+
+
+def _rows(layer, x):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [rows][k]")
+    _need(x, "x", _F32, (x.shape[0], layer.k), layer.device)
+    return x.shape[0]
+
+
+def _work(layer, rows, workspace, own):
+    if workspace is None:
+        workspace = layer.workspace(rows)
+        own.append(workspace)
+    elif workspace.dtype != _U8 or workspace.device != layer.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the layer's device")
+    return workspace
+
+
+def _out(t, name, dtype, shape, layer, own):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=layer.device)
+        own.append(t)
+    else:
+        _need(t, name, dtype, shape, layer.device)
+    return t
+
+
+def moe_route(layer: MoeLayer, x: torch.Tensor, ids=None, gates=None, workspace=None, stream=None):
+    """(ids int32, gates f32) [rows][top_k] that the layer's router chooses."""
+    rows, own = _rows(layer, x), []
+    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
+    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
+    workspace = _work(layer, rows, workspace, own)
+    _call("q8_moe_route", layer.device, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(), gates.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return ids, gates
+
+
+def moe_experts(layer: MoeLayer, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, residual=None, out=None,
+                workspace=None, stream=None) -> torch.Tensor:
+    """y [rows][k] = residual + the gated sum of the given experts (ids outside the layer add nothing)."""
+    rows, own = _rows(layer, x), []
+    _need(ids, "ids", _I32, (rows, layer.top_k), layer.device)
+    _need(gates, "gates", _F32, (rows, layer.top_k), layer.device)
+    if residual is not None:
+        _need(residual, "residual", _F32, (rows, layer.k), layer.device)
+    out = _out(out, "out", _F32, (rows, layer.k), layer, own)
+    workspace = _work(layer, rows, workspace, own)
+    _call("q8_moe_experts", layer.device, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(),
+          gates.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return out
+
+
+def moe(layer: MoeLayer, x: torch.Tensor, residual=None, out=None, ids=None, gates=None, workspace=None, stream=None):
+    """(y [rows][k], ids, gates): the whole layer, router and experts."""
+    rows, own = _rows(layer, x), []
+    if residual is not None:
+        _need(residual, "residual", _F32, (rows, layer.k), layer.device)
+    out = _out(out, "out", _F32, (rows, layer.k), layer, own)
+    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
+    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
+    workspace = _work(layer, rows, workspace, own)
+    _call("q8_moe", layer.device, stream, own, layer._ref, x.data_ptr(), rows,
+          None if residual is None else residual.data_ptr(), out.data_ptr(), ids.data_ptr(), gates.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return out, ids, gates
