@@ -89,6 +89,52 @@ q8_status q8_moe_experts(const q8_moe_layer *layer, const float *x, int64_t rows
 q8_status q8_moe(const q8_moe_layer *layer, const float *x, int64_t rows, const float *residual, float *y,
                  int32_t *ids, float *gates, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The next token
+ *
+ * Draws one token from each row of logits with given parameters and a given
+ * random number, the counterpart of q8_matvec_argmax for sampled decoding.  A
+ * row's candidates are its logits that are neither NaN nor -inf.  With m the
+ * largest of them (T the row's temperature):
+ *
+ *   w_i = floor(exp((l_i - m) * (1/T)) * 2^44 + 1/2)   exp, product and quotient in f64
+ *
+ * an integer weight, so that every sum below is exact.  In descending order of
+ * the logits, the lowest index first among equals, with running sums C_j:
+ *
+ *   top-k : the first top_k tokens; top_k <= 0 (or NULL): all
+ *   top-p : the shortest prefix with C_j >= top_p * C_top-k (at least one token);
+ *           top_p >= 1, NaN or NULL: all
+ *   min-p : the tokens with w_i >= min_p * 2^44 (at least one); min_p <= 0, NaN or
+ *           NULL: all
+ *
+ * The shortest of the three prefixes is kept, W is its sum, and the token is the
+ * first with C_j > u * W (the last kept one of non-zero weight if there is none).
+ * Products and comparisons of sums are in f64.  prob = w / W.  T <= 0 or NaN: the
+ * largest logit, the lowest index among equals, prob 1.  A row without
+ * candidates: index -1, prob 0.
+ *
+ *   logits      : f32 [rows] rows of n values, `ld` values apart (ld >= n), 4-byte
+ *                 aligned.
+ *   temperature : f32 [rows], or NULL: 1.
+ *   top_k       : int32 [rows] or NULL;  top_p, min_p : f32 [rows] or NULL.
+ *   u           : f32 [rows], the random numbers, in [0, 1).
+ *   idx         : out, int32 [rows];  prob : out, f32 [rows], or NULL.
+ *   workspace   : 16-byte aligned, at least q8_sample_workspace_bytes, zero-filled
+ *                 by the caller before its first use; every call leaves its
+ *                 counters at zero again, so it serves call after call of any
+ *                 sizes.  Calls in flight at once must not share one.
+ * All arrays 4-byte aligned; the outputs and the workspace must not overlap any
+ * other argument.  Limits (else Q8_E_SHAPE): 1 <= n < 2^19, 0 <= rows <= 65536.
+ * Errors: Q8_E_NULL, Q8_E_SHAPE, Q8_E_ALIGN, Q8_E_ALIAS, Q8_E_HIP.
+ * ------------------------------------------------------------------------- */
+q8_status q8_sample(const float *logits, int64_t ld, int64_t rows, int64_t n, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *idx,
+                    float *prob, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of the q8_sample workspace (0 for sizes it refuses). */
+int64_t q8_sample_workspace_bytes(int64_t rows, int64_t n);
+
 #ifdef __cplusplus
 }
 #endif

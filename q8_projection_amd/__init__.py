@@ -51,6 +51,8 @@ SIGNATURES = {
     "q8_moe_route": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _P]),
     "q8_moe_experts": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
     "q8_moe": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "q8_sample": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "q8_sample_workspace_bytes": (_I64, [_I64, _I64]),
 }
 
 _lib = None
@@ -323,4 +325,4 @@ def block_sums(mode, w: torch.Tensor, n: int, k: int, hi, lo=None, out=None, row
     return out
 
 
-from .decode import MoeLayer, moe, moe_experts, moe_route, moe_workspace_bytes  # noqa: E402
+from .decode import MoeLayer, moe, moe_experts, moe_route, moe_workspace_bytes, sample, sample_workspace_bytes  # noqa: E402

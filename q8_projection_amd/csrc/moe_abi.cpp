@@ -9,25 +9,13 @@
 
 #include "../../include/q8_decode.h"
 #include "moe.h"
+#include "ranges.h"
 
 namespace {
 
 constexpr int64_t kMaxDim = 65536;                    // k and ff
 constexpr int64_t kMaxLayerBlocks = int64_t(1) << 31;  // blocks of one of the three matrices (73 GB)
 constexpr int64_t kMaxRows = int64_t(1) << 20;
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    const void *p;
-    int64_t bytes;
-};
-
-bool overlap(const Range &a, const Range &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
-}
 
 q8_status check_layer(const q8_moe_layer *l, int64_t rows) {
     if (!l) return Q8_E_NULL;
@@ -62,29 +50,29 @@ q8_status moe(const q8_moe_layer *l, const float *x, int64_t rows, const float *
     if (!x || !ids || !gates || !workspace) return Q8_E_NULL;
     if (route && !l->router) return Q8_E_NULL;
     if (experts && (!l->w_gate || !l->w_up || !l->w_down || !y)) return Q8_E_NULL;
-    if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(gates, 4) || !aligned(workspace, 16)) return Q8_E_ALIGN;
-    if (route && !aligned(l->router, 16)) return Q8_E_ALIGN;
-    if (experts && (!aligned(l->w_gate, 4) || !aligned(l->w_up, 4) || !aligned(l->w_down, 4) || !aligned(y, 4) ||
-                    !aligned(residual, 4)))
+    if (!q8::aligned_to(x, 16) || !q8::aligned_to(ids, 4) || !q8::aligned_to(gates, 4) || !q8::aligned_to(workspace, 16)) return Q8_E_ALIGN;
+    if (route && !q8::aligned_to(l->router, 16)) return Q8_E_ALIGN;
+    if (experts && (!q8::aligned_to(l->w_gate, 4) || !q8::aligned_to(l->w_up, 4) || !q8::aligned_to(l->w_down, 4) || !q8::aligned_to(y, 4) ||
+                    !q8::aligned_to(residual, 4)))
         return Q8_E_ALIGN;
     const int64_t need = q8_moe_workspace_bytes(l, rows);
     if (workspace_bytes < need) return Q8_E_SHAPE;
     const int64_t wbytes = int64_t(l->n_experts) * l->ff * (l->k / 32) * 34;
-    const Range rx{x, rows * l->k * 4}, ry{experts ? y : nullptr, rows * l->k * 4},
+    const q8::Range rx{x, rows * l->k * 4}, ry{experts ? y : nullptr, rows * l->k * 4},
         rres{experts ? residual : nullptr, rows * l->k * 4}, rids{ids, rows * l->top_k * 4},
         rgates{gates, rows * l->top_k * 4}, rws{workspace, need},
         rr{route ? l->router : nullptr, int64_t(l->n_experts) * l->k * 4},
         rg{experts ? l->w_gate : nullptr, wbytes}, ru{experts ? l->w_up : nullptr, wbytes},
         rd{experts ? l->w_down : nullptr, wbytes};
-    const Range inputs[] = {rx, rr, rg, ru, rd};
-    for (const Range &in : inputs)
-        if (overlap(ry, in) || overlap(rws, in) || (route && (overlap(rids, in) || overlap(rgates, in))))
+    const q8::Range inputs[] = {rx, rr, rg, ru, rd};
+    for (const q8::Range &in : inputs)
+        if (q8::overlaps(ry, in) || q8::overlaps(rws, in) || (route && (q8::overlaps(rids, in) || q8::overlaps(rgates, in))))
             return Q8_E_ALIAS;
-    if (overlap(ry, rids) || overlap(ry, rgates) || overlap(rws, ry) || overlap(rws, rres) || overlap(rws, rids) ||
-        overlap(rws, rgates))
+    if (q8::overlaps(ry, rids) || q8::overlaps(ry, rgates) || q8::overlaps(rws, ry) || q8::overlaps(rws, rres) || q8::overlaps(rws, rids) ||
+        q8::overlaps(rws, rgates))
         return Q8_E_ALIAS;
-    if (route && (overlap(rids, rgates) || overlap(rids, rres) || overlap(rgates, rres))) return Q8_E_ALIAS;
-    if (residual != y && overlap(ry, rres)) return Q8_E_ALIAS;
+    if (route && (q8::overlaps(rids, rgates) || q8::overlaps(rids, rres) || q8::overlaps(rgates, rres))) return Q8_E_ALIAS;
+    if (residual != y && q8::overlaps(ry, rres)) return Q8_E_ALIAS;
     for (int64_t r0 = 0; r0 < rows; r0 += q8::kMoeSlice) {
         q8::MoeArgs a = sizes_of(l, static_cast<int>(std::min<int64_t>(q8::kMoeSlice, rows - r0)));
         q8::moe_layout(a, static_cast<uint8_t *>(workspace), l->mode);

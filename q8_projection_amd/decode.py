@@ -1,4 +1,5 @@
-"""Python binding of include/q8_decode.h: the mixture-of-experts layer.
+"""Python binding of include/q8_decode.h: the mixture-of-experts layer and the
+sampler.
 
 As in the package's other wrappers, argument marshalling only.  Every tensor of
 a call lives on one device, and the call runs on that device whichever is
@@ -37,7 +38,7 @@ def _need(t, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _call(fn: str, device, stream, own, *args):
+def _call(fn: str, device, rows: int, stream, own, *args):
     """Call a library function on `device` and `stream` (None: its current
     stream).  `own`: tensors allocated here, which the caching allocator must
     not hand out again before the stream is done with them."""
@@ -55,6 +56,8 @@ def _call(fn: str, device, stream, own, *args):
             for t in own:
                 if t is not None:
                     t.record_stream(ext)
+    if rows == 0:
+        return  # an empty tensor has no address; there is nothing to enqueue
     f = getattr(_q8.lib(), fn)
     if torch.cuda.current_device() == device.index:
         status = f(*args, raw)
@@ -63,6 +66,10 @@ def _call(fn: str, device, stream, own, *args):
             status = f(*args, raw)
     if status != 0:
         raise _q8.Q8Error(fn, status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 class MoeLayer:
@@ -144,7 +151,7 @@ def moe_route(layer: MoeLayer, x: torch.Tensor, ids=None, gates=None, workspace=
     ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
     gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
     workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe_route", layer.device, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(), gates.data_ptr(),
+    _call("q8_moe_route", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(), gates.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return ids, gates
 
@@ -159,8 +166,8 @@ def moe_experts(layer: MoeLayer, x: torch.Tensor, ids: torch.Tensor, gates: torc
         _need(residual, "residual", _F32, (rows, layer.k), layer.device)
     out = _out(out, "out", _F32, (rows, layer.k), layer, own)
     workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe_experts", layer.device, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(),
-          gates.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+    _call("q8_moe_experts", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(),
+          gates.data_ptr(), _ptr(residual), out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
     return out
 
@@ -174,7 +181,51 @@ def moe(layer: MoeLayer, x: torch.Tensor, residual=None, out=None, ids=None, gat
     ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
     gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
     workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe", layer.device, stream, own, layer._ref, x.data_ptr(), rows,
-          None if residual is None else residual.data_ptr(), out.data_ptr(), ids.data_ptr(), gates.data_ptr(),
+    _call("q8_moe", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows,
+          _ptr(residual), out.data_ptr(), ids.data_ptr(), gates.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return out, ids, gates
+
+
+def sample_workspace_bytes(rows: int, n: int) -> int:
+    """Bytes of the sample workspace for `rows` rows of `n` logits (0: refused)."""
+    return int(_q8.lib().q8_sample_workspace_bytes(rows, n))
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, idx=None,
+           prob=None, workspace=None, stream=None):
+    """(idx int32 [rows], prob f32 [rows]): one token drawn from each row of f32
+    logits [rows][n] with the random numbers u f32 [rows].
+
+    logits may have any row stride (a view of a wider buffer).  temperature,
+    top_p, min_p (f32 [rows]) and top_k (int32 [rows]) are device tensors, or None
+    where the filter is off.  The workspace (uint8, at least
+    sample_workspace_bytes) must start zero-filled and may be kept.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype != _F32 or not logits.is_cuda:
+        raise ValueError("logits must be a f32 device tensor [rows][n]")
+    rows, n = logits.shape
+    if n > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit stride within a row")
+    ld = logits.stride(0) if rows > 1 else n
+    dev, own = logits.device, []
+    for t, name, dtype in ((u, "u", _F32), (temperature, "temperature", _F32), (top_k, "top_k", _I32),
+                           (top_p, "top_p", _F32), (min_p, "min_p", _F32), (idx, "idx", _I32), (prob, "prob", _F32)):
+        if t is not None:
+            _need(t, name, dtype, (rows,), dev)
+    if u is None:
+        raise ValueError("u is required")
+    if idx is None:
+        idx = torch.empty(rows, dtype=_I32, device=dev)
+        own.append(idx)
+    if prob is None:
+        prob = torch.empty(rows, dtype=_F32, device=dev)
+        own.append(prob)
+    if workspace is None:
+        workspace = torch.zeros(sample_workspace_bytes(rows, n), dtype=_U8, device=dev)
+        own.append(workspace)
+    elif workspace.dtype != _U8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
+    _call("q8_sample", dev, rows, stream, own, logits.data_ptr(), ld, rows, n, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+          _ptr(min_p), u.data_ptr(), idx.data_ptr(), prob.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return idx, prob

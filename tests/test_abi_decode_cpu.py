@@ -106,3 +106,27 @@ def test_overlaps():
         assert moe(layer(), **kw) == ALIAS, kw
     assert route(layer(), ids=gates + 4) == ALIAS
     assert experts(layer(), y=gates) == ALIAS
+
+
+def sample(logits=BASE, ld=1000, rows=4, n=1000, t=BASE + 16 * MB, k=BASE + 17 * MB, p=BASE + 18 * MB, mp=BASE + 19 * MB,
+           u=BASE + 20 * MB, idx=BASE + 21 * MB, prob=BASE + 22 * MB, ws=BASE + 32 * MB, wsb=1 << 30):
+    return q8.lib().q8_sample(logits, ld, rows, n, t, k, p, mp, u, idx, prob, ws, wsb, None)
+
+
+def test_sample_refusals():
+    assert sample(rows=0) == OK
+    size = q8.lib().q8_sample_workspace_bytes
+    assert 0 < size(1, 1) <= size(4, 1000) < size(64, 151936)
+    assert size(-1, 5) == size(1, 0) == size(1, 1 << 19) == size(65537, 1) == 0
+    for kw in (dict(n=0), dict(n=-1), dict(n=1 << 19, ld=1 << 20), dict(ld=999), dict(rows=-1), dict(rows=65537),
+               dict(rows=1 << 62), dict(ld=1 << 62), dict(wsb=size(4, 1000) - 1)):
+        assert sample(**kw) == SHAPE, kw
+    for kw in (dict(logits=None), dict(u=None), dict(idx=None), dict(ws=None)):
+        assert sample(**kw) == NULL, kw
+    for kw in (dict(logits=BASE + 2), dict(t=BASE + 16 * MB + 1), dict(k=BASE + 17 * MB + 2), dict(p=BASE + 18 * MB + 3),
+               dict(mp=BASE + 19 * MB + 2), dict(u=BASE + 20 * MB + 1), dict(idx=BASE + 21 * MB + 2),
+               dict(prob=BASE + 22 * MB + 2), dict(ws=BASE + 32 * MB + 8)):
+        assert sample(**kw) == ALIGN, kw
+    for kw in (dict(idx=BASE + 4 * 3999), dict(prob=BASE), dict(idx=BASE + 20 * MB), dict(prob=BASE + 21 * MB + 12),
+               dict(ws=BASE), dict(ws=BASE + 21 * MB), dict(idx=BASE + 17 * MB + 4)):
+        assert sample(**kw) == ALIAS, kw
