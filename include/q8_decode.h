@@ -97,9 +97,9 @@ q8_status q8_moe(const q8_moe_layer *layer, const float *x, int64_t rows, const 
  * row's candidates are its logits that are neither NaN nor -inf.  With m the
  * largest of them (T the row's temperature):
  *
- *   w_i = floor(exp((l_i - m) * (1/T)) * 2^44 + 1/2)   exp, product and quotient in f64
+ *   w_i = exp((l_i - m) * (1/T)) * 2^44, in f64, rounded to a whole number
  *
- * an integer weight, so that every sum below is exact.  In descending order of
+ * so that every sum below is exact.  In descending order of
  * the logits, the lowest index first among equals, with running sums C_j:
  *
  *   top-k : the first top_k tokens; top_k <= 0 (or NULL): all
@@ -120,10 +120,9 @@ q8_status q8_moe(const q8_moe_layer *layer, const float *x, int64_t rows, const 
  *   top_k       : int32 [rows] or NULL;  top_p, min_p : f32 [rows] or NULL.
  *   u           : f32 [rows], the random numbers, in [0, 1).
  *   idx         : out, int32 [rows];  prob : out, f32 [rows], or NULL.
- *   workspace   : 16-byte aligned, at least q8_sample_workspace_bytes, zero-filled
- *                 by the caller before its first use; every call leaves its
- *                 counters at zero again, so it serves call after call of any
- *                 sizes.  Calls in flight at once must not share one.
+ *   workspace   : 16-byte aligned, at least q8_sample_workspace_bytes; scratch,
+ *                 which need not be cleared.  Calls in flight at once must not
+ *                 share one.
  * All arrays 4-byte aligned; the outputs and the workspace must not overlap any
  * other argument.  Limits (else Q8_E_SHAPE): 1 <= n < 2^19, 0 <= rows <= 65536.
  * Errors: Q8_E_NULL, Q8_E_SHAPE, Q8_E_ALIGN, Q8_E_ALIAS, Q8_E_HIP.

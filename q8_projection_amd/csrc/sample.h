@@ -4,10 +4,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace q8 {
 
 constexpr int64_t kSampleMaxN = (int64_t(1) << 19) - 1;  // sums of n weights of at most 2^44 fit 63 bits
 constexpr int64_t kSampleMaxRows = int64_t(1) << 16;
+constexpr int kSampleSlice = 1024;  // rows of one pass (a histogram each in the workspace)
 constexpr int kSubBlock = 64;                            // logits per stored maximum
 
 struct SampleArgs {
@@ -22,15 +25,60 @@ struct SampleArgs {
     const float *u;            // [rows]
     int32_t *idx;              // [rows]
     float *prob;               // [rows] or null
-    float *submax;             // workspace [rows][nsub]
-    int nsub;
+    int nsub;                  // maxima a row
+    int segments;              // workgroups that share a row's histogram
+    // workspace
+    struct RowState *state;    // [rows]
+    unsigned long long *sums;  // [rows][segments][kSampleSums]: the segments' histograms
+    unsigned long long *near;  // [rows][kNear]: gathered tokens
+    int gathers;               // workgroups that gather a row's tokens, a power of two
+    float *submax;             // [rows][nsub]
+    float *wavemax;            // [rows][nwave]: maxima of 1024 logits
+    int nwave;
+    int segment;               // logits of one segment
 };
+
+// How far a row is (cleared by the first kernel of a call).
+struct RowState {
+    uint32_t phase;    // 0: every segment has its histogram; 1: drawn; 2: segment 0 has the whole row's
+    uint32_t fill;     // tokens gathered
+    uint32_t arrived;  // workgroups that have gathered
+    uint32_t pad;
+};
+
+constexpr int kNear = 1024;
+constexpr int kSampleBins = 2048;
+// a histogram: weight sums of the bins, counts of the bins (32 bits each),
+// and the sum of the weights that min-p keeps
+constexpr int kSampleSums = kSampleBins + kSampleBins / 2 + 1;
+constexpr int kSegment = 4096;  // logits one workgroup adds up, at least
+constexpr int kMaxWgLogits = 4096;  // logits of one workgroup of the maxima's kernel, 1024 a wave
 
 // Places the workspace's parts (base may be null: sizes only); returns its bytes.
 inline int64_t sample_layout(SampleArgs &a, uint8_t *base) {
     a.nsub = (a.n + kSubBlock - 1) / kSubBlock;
-    a.submax = reinterpret_cast<float *>(base);
-    return (static_cast<int64_t>(a.rows) * a.nsub * 4 + 255) / 256 * 256;
+    // Enough segments for two workgroups a CU, no more: each costs the row's
+    // maximum, an empty histogram and the reading of its own by the last kernel.
+    const int most = std::min(16, (a.n + kSegment - 1) / kSegment);
+    const int want = a.rows > 0 ? (512 + a.rows - 1) / a.rows : 1;
+    a.segments = std::min(want, most);
+    a.segment = ((a.n + a.segments - 1) / a.segments + kSegment - 1) / kSegment * kSegment;
+    a.segments = (a.n + a.segment - 1) / a.segment;
+    a.nwave = (a.n + kMaxWgLogits - 1) / kMaxWgLogits * 4;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t *p = base ? base + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    a.gathers = 1;
+    while (a.gathers < 8 && 2 * a.gathers * a.rows <= 256 && a.n / a.gathers > 65536) a.gathers *= 2;
+    a.state = reinterpret_cast<RowState *>(take(sizeof(RowState) * int64_t(a.rows)));
+    a.sums = reinterpret_cast<unsigned long long *>(take(8 * kSampleSums * int64_t(a.rows) * a.segments));
+    a.near = reinterpret_cast<unsigned long long *>(take(a.gathers > 1 ? 8 * kNear * int64_t(a.rows) : 0));
+    a.submax = reinterpret_cast<float *>(take(int64_t(4) * a.rows * a.nsub));
+    a.wavemax = reinterpret_cast<float *>(take(int64_t(4) * a.rows * a.nwave));
+    return at;
 }
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/q8_decode.h"
 #include "ranges.h"
 #include "sample.h"
@@ -12,7 +14,7 @@ extern "C" {
 int64_t q8_sample_workspace_bytes(int64_t rows, int64_t n) {
     if (rows < 0 || rows > q8::kSampleMaxRows || n < 1 || n > q8::kSampleMaxN) return 0;
     q8::SampleArgs a = {};
-    a.rows = static_cast<int>(rows);
+    a.rows = static_cast<int>(std::min<int64_t>(rows, q8::kSampleSlice));
     a.n = static_cast<int>(n);
     return q8::sample_layout(a, nullptr);
 }
@@ -42,20 +44,23 @@ q8_status q8_sample(const float *logits, int64_t ld, int64_t rows, int64_t n, co
             if (q8::overlaps(outs[i], outs[j])) return Q8_E_ALIAS;
     }
     if (rows == 0) return Q8_OK;
-    q8::SampleArgs a = {};
-    a.logits = logits;
-    a.ld = ld;
-    a.n = static_cast<int>(n);
-    a.rows = static_cast<int>(rows);
-    a.temperature = temperature;
-    a.top_k = top_k;
-    a.top_p = top_p;
-    a.min_p = min_p;
-    a.u = u;
-    a.idx = idx;
-    a.prob = prob;
-    q8::sample_layout(a, static_cast<uint8_t *>(workspace));
-    return q8::launch_sample(a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? Q8_OK : Q8_E_HIP;
+    for (int64_t r0 = 0; r0 < rows; r0 += q8::kSampleSlice) {
+        q8::SampleArgs a = {};
+        a.logits = logits + r0 * ld;
+        a.ld = ld;
+        a.n = static_cast<int>(n);
+        a.rows = static_cast<int>(std::min<int64_t>(rows - r0, q8::kSampleSlice));
+        a.temperature = temperature ? temperature + r0 : nullptr;
+        a.top_k = top_k ? top_k + r0 : nullptr;
+        a.top_p = top_p ? top_p + r0 : nullptr;
+        a.min_p = min_p ? min_p + r0 : nullptr;
+        a.u = u + r0;
+        a.idx = idx + r0;
+        a.prob = prob ? prob + r0 : nullptr;
+        q8::sample_layout(a, static_cast<uint8_t *>(workspace));
+        if (q8::launch_sample(a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess) return Q8_E_HIP;
+    }
+    return Q8_OK;
 }
 
 }  // extern "C"

@@ -200,7 +200,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     logits may have any row stride (a view of a wider buffer).  temperature,
     top_p, min_p (f32 [rows]) and top_k (int32 [rows]) are device tensors, or None
     where the filter is off.  The workspace (uint8, at least
-    sample_workspace_bytes) must start zero-filled and may be kept.
+    sample_workspace_bytes) is scratch and may be kept from call to call.
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype != _F32 or not logits.is_cuda:
         raise ValueError("logits must be a f32 device tensor [rows][n]")
@@ -222,7 +222,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
         prob = torch.empty(rows, dtype=_F32, device=dev)
         own.append(prob)
     if workspace is None:
-        workspace = torch.zeros(sample_workspace_bytes(rows, n), dtype=_U8, device=dev)
+        workspace = torch.empty(sample_workspace_bytes(rows, n), dtype=_U8, device=dev)
         own.append(workspace)
     elif workspace.dtype != _U8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")

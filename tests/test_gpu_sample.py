@@ -167,3 +167,18 @@ def test_empty_and_refused():
         q8.sample(l[:1].expand(2, 10), u)
     with pytest.raises(q8.Q8Error, match="Q8_E_SHAPE"):
         q8.sample(l, u, workspace=torch.zeros(0, dtype=torch.uint8, device="cuda").new_zeros(16))
+
+
+def test_more_rows_than_one_pass_takes():
+    rows, n = 2100, 300
+    rng = np.random.default_rng(8)
+    check(logits_of(rows, n, 9), temperature=rng.choice([0.0, 0.8, 1.5], rows), top_k=rng.choice([0, 4, 290], rows),
+          top_p=rng.choice([0.3, 1.0], rows))
+
+
+@pytest.mark.parametrize("rows,n", [(1, 262144), (2, 524287), (20, 70001)])
+def test_long_rows(rows, n):
+    say("long rows", rows, n)
+    l = logits_of(rows, n, n)
+    for kw in (dict(), dict(top_p=0.95), dict(top_k=1500, top_p=0.9), dict(top_k=100), dict(temperature=2.0, min_p=0.01)):
+        check(l, what=kw, **kw)
