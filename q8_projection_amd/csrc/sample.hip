@@ -797,7 +797,8 @@ __device__ __forceinline__ float largest(Shared &s, const SampleArgs &a, int row
     if ((tid & 63) == 0) s.wave[tid >> 6] = __float_as_uint(m);
     __syncthreads();
     m = __uint_as_float(static_cast<uint32_t>(s.wave[tid & (kWaves - 1)]));
-    return row_max(m);  // 16 waves: every row of 16 lanes holds them all
+    m = row_max(m);  // 16 waves: every row of 16 lanes holds them all
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m)));  // the same for every lane: a scalar
 }
 
 __device__ __forceinline__ Row row_of(const SampleArgs &a, int row, float t, float m) {
