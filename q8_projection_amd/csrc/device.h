@@ -105,6 +105,28 @@ __device__ __forceinline__ double dpp_f64(double v) {
                                           static_cast<uint32_t>(lo));
 }
 
+// One DPP move of a float.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+
+// Maximum over each 16 lanes (NaN loses).
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp_f32<0xb1>(v));      // quad_perm [1,0,3,2]
+    v = fmaxf(v, dpp_f32<0x4e>(v));      // quad_perm [2,3,0,1]
+    v = fmaxf(v, dpp_f32<0x141>(v));     // row_half_mirror
+    return fmaxf(v, dpp_f32<0x140>(v));  // row_mirror
+}
+
+// Maximum over the 64 lanes of a wave; every lane gets it.
+__device__ __forceinline__ float wave_max(float v) {
+    const int b = __builtin_bit_cast(int, row_max(v));
+    const auto at = [&](int lane) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, lane)); };
+    return fmaxf(fmaxf(at(0), at(16)), fmaxf(at(32), at(48)));
+}
+
 __device__ __forceinline__ double readlane_f64(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);

@@ -41,19 +41,11 @@ __device__ __forceinline__ ActSource act_source(const void *words, const float *
     return s;
 }
 
-// A tile of up to 8 rows of one expert's matrix, as a range-checked buffer.
-struct WeightTile {
-    __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t row_part;  // byte offset of the lane's row
-};
-
-__device__ __forceinline__ WeightTile weight_tile(const uint8_t *w, int64_t first_row, int nb, int lane) {
-    WeightTile t;
+// A tile of 8 rows of one expert's matrix, as a range-checked buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_tile(const uint8_t *w, int64_t first_row, int nb) {
     const uint32_t row_bytes = static_cast<uint32_t>(nb) * kBlockBytes;
-    t.rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(w + first_row * row_bytes), 0,
-                                               static_cast<int>(kTileRows * row_bytes), kBufferDword3);
-    t.row_part = (lane >> 3) * row_bytes;
-    return t;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(w + first_row * row_bytes), 0,
+                                             static_cast<int>(kTileRows * row_bytes), kBufferDword3);
 }
 
 template <int WORDS, int TG>
@@ -63,40 +55,70 @@ struct Step {
     float s[TG];
 };
 
-// Loads of step `st` (blocks 8 st .. 8 st + 7): nothing is read past nb blocks
-// or for a token with base row -1 (zeros arrive instead).
+// Where a lane's loads of the next step are: its weight window (row lane / 8, block
+// lane % 8 of the step), its piece of each token's words (block lane / 8), and its
+// block's scales.  All move by a constant per step; from `w_end` and `a_end` on the
+// lane's blocks are behind the row's last or behind the wave's steps, and the loads
+// read zeros and touch no memory.
 template <int WORDS, int TG>
-__device__ __forceinline__ void issue(const WeightTile &wt, const ActSource &src, const int (&arow)[TG], int st,
-                                      bool live, int lane, Step<WORDS, TG> &out) {
-    constexpr int D = kActDwords<WORDS>;
-    const int b = st * kStepBlocks + (lane & 7);  // the lane's weight block
-    const uint32_t off = (wt.row_part + (static_cast<uint32_t>(b * kBlockBytes) & ~3u)) | oob_bit(live && b < src.nb);
-    const u32x4 d0 = __builtin_amdgcn_raw_buffer_load_b128(wt.rsrc, off, 0, 0);
-    const u32x4 d1 = __builtin_amdgcn_raw_buffer_load_b128(wt.rsrc, off + 16, 0, 0);
-    out.w.d[8] = __builtin_amdgcn_raw_buffer_load_b32(wt.rsrc, off + 32, 0, 0);
-    out.w.d[0] = d0.x; out.w.d[1] = d0.y; out.w.d[2] = d0.z; out.w.d[3] = d0.w;
-    out.w.d[4] = d1.x; out.w.d[5] = d1.y; out.w.d[6] = d1.z; out.w.d[7] = d1.w;
-    const int ab = st * kStepBlocks + (lane >> 3);  // the block whose words the lane carries
+struct Stream {
+    __amdgpu_buffer_rsrc_t tile, words, scales;
+    uint32_t w_off, a_off[TG], s_off[TG];
+    int step, w_end, a_end;
+
+    static constexpr int D = kActDwords<WORDS>;
+
+    __device__ __forceinline__ Stream(__amdgpu_buffer_rsrc_t weights, const ActSource &src, const int (&arow)[TG], int st0,
+                                      int st1, int lane) {
+        tile = weights;
+        words = src.words;
+        scales = src.scales;
+        step = st0;
+        // the first step at which 8 step + (lane's block) >= nb
+        w_end = min(st1, (src.nb - (lane & 7) + kStepBlocks - 1) / kStepBlocks);
+        a_end = min(st1, (src.nb - (lane >> 3) + kStepBlocks - 1) / kStepBlocks);
+        w_off = (lane >> 3) * static_cast<uint32_t>(src.nb) * kBlockBytes + st0 * (kStepBlocks * kBlockBytes) +
+                (((lane & 7) * kBlockBytes) & ~3u);
 #pragma unroll
-    for (int t = 0; t < TG; ++t) {
-        const bool ok = live && arow[t] >= 0;
-        const uint32_t row = static_cast<uint32_t>(arow[t]) * src.nb;
-        const uint32_t ao = ((row + ab) * (32 * D) + (lane & 7) * (4 * D)) | oob_bit(ok && ab < src.nb);
-        if constexpr (D == 1) {
-            out.a[t][0] = __builtin_amdgcn_raw_buffer_load_b32(src.words, ao, 0, 0);
-        } else if constexpr (D == 2) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.words, ao, 0, 0);
-            out.a[t][0] = v.x;
-            out.a[t][1] = v.y;
-        } else {
-            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.words, ao, 0, 0);
-            out.a[t][0] = v.x; out.a[t][1] = v.y; out.a[t][2] = v.z; out.a[t][3] = v.w;
+        for (int t = 0; t < TG; ++t) {
+            const uint32_t block = static_cast<uint32_t>(arow[t]) * src.nb + st0 * kStepBlocks;
+            const uint32_t dead = oob_bit(arow[t] >= 0);
+            a_off[t] = ((block + (lane >> 3)) * (32 * D) + (lane & 7) * (4 * D)) | dead;
+            s_off[t] = ((block + (lane & 7)) * 4) | dead;
         }
-        if constexpr (WORDS > 0)
-            out.s[t] = __uint_as_float(
-                __builtin_amdgcn_raw_buffer_load_b32(src.scales, ((row + b) * 4) | oob_bit(ok && b < src.nb), 0, 0));
     }
-}
+
+    __device__ __forceinline__ void next(Step<WORDS, TG> &out) {
+        const uint32_t w_dead = oob_bit(step < w_end), a_dead = oob_bit(step < a_end);
+        const uint32_t off = w_off | w_dead;
+        const u32x4 d0 = __builtin_amdgcn_raw_buffer_load_b128(tile, off, 0, 0);
+        const u32x4 d1 = __builtin_amdgcn_raw_buffer_load_b128(tile, off + 16, 0, 0);
+        out.w.d[8] = __builtin_amdgcn_raw_buffer_load_b32(tile, off + 32, 0, 0);
+        out.w.d[0] = d0.x; out.w.d[1] = d0.y; out.w.d[2] = d0.z; out.w.d[3] = d0.w;
+        out.w.d[4] = d1.x; out.w.d[5] = d1.y; out.w.d[6] = d1.z; out.w.d[7] = d1.w;
+        w_off += kStepBlocks * kBlockBytes;
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+            const uint32_t ao = a_off[t] | a_dead;
+            if constexpr (D == 1) {
+                out.a[t][0] = __builtin_amdgcn_raw_buffer_load_b32(words, ao, 0, 0);
+            } else if constexpr (D == 2) {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(words, ao, 0, 0);
+                out.a[t][0] = v.x;
+                out.a[t][1] = v.y;
+            } else {
+                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(words, ao, 0, 0);
+                out.a[t][0] = v.x; out.a[t][1] = v.y; out.a[t][2] = v.z; out.a[t][3] = v.w;
+            }
+            a_off[t] += kStepBlocks * 32 * D;
+            if constexpr (WORDS > 0) {
+                out.s[t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales, s_off[t] | w_dead, 0, 0));
+                s_off[t] += kStepBlocks * 4;
+            }
+        }
+        ++step;
+    }
+};
 
 // acc[t] += the step's block terms of the lane's row and block.
 template <int WORDS, int TG>
@@ -161,87 +183,120 @@ __device__ __forceinline__ double row_sum(double v) {
 
 // Steps [st0, st1) of one tile and TG tokens, P steps in flight.
 template <int WORDS, int TG, int P>
-__device__ __forceinline__ void run_steps(const WeightTile &wt, const ActSource &src, const int (&arow)[TG], int st0,
+__device__ __forceinline__ void run_steps(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int (&arow)[TG], int st0,
                                           int st1, uint8_t *buf, int lane, double (&acc)[TG]) {
+    Stream<WORDS, TG> stream(wt, src, arow, st0, st1, lane);
     Step<WORDS, TG> ring[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) issue<WORDS, TG>(wt, src, arow, st0 + p, st0 + p < st1, lane, ring[p]);
+    for (int p = 0; p < P; ++p) stream.next(ring[p]);
+#pragma clang loop unroll(disable)
     for (int s0 = st0; s0 < st1; s0 += P) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             compute<WORDS, TG>(ring[p], buf, lane, acc);
-            issue<WORDS, TG>(wt, src, arow, s0 + p + P, s0 + p + P < st1, lane, ring[p]);
+            stream.next(ring[p]);
+            __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time in registers
         }
     }
 }
 
-constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves
+constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves, at most
 
+// Steps in flight for a pass of TG tokens: as many loads ahead as registers allow at
+// two workgroups a CU.
+template <int TG>
+constexpr int kAhead = TG == 4 ? 2 : TG == 2 ? 3 : 4;
+// (one workgroup a CU in the f32 mode, whose conversions need the registers)
 template <int WORDS>
-constexpr int kWaveBuf = kTokenGroup * kStepBlocks * 32 * kActDwords<WORDS>;
+constexpr int kWavesPerSimd = WORDS == 0 ? 2 : 4;
+
+// One pass over steps [st0, st1) of a tile for tokens rows[0 .. n) (n at most
+// kTokenGroup): f(token, total over the lanes of a row).
+template <int WORDS, int TG, typename F>
+__device__ __forceinline__ void pass_of(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int *rows, int n, int st0,
+                                        int st1, uint8_t *buf, int lane, F f) {
+    int arow[TG];
+    double acc[TG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+        arow[t] = t < n ? rows[t] : -1;
+        acc[t] = 0.0;
+    }
+    run_steps<WORDS, TG, kAhead<TG>>(wt, src, arow, st0, st1, buf, lane, acc);
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+        if (t < n) f(t, row_sum(acc[t]) * (WORDS == 2 ? 1.0 / 128.0 : 1.0));
+}
+
+template <int WORDS, int MAX_TG, typename F>
+__device__ __forceinline__ void pass(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int *rows, int n, int st0,
+                                     int st1, uint8_t *buf, int lane, F f) {
+    if (MAX_TG == 1 || n == 1)
+        pass_of<WORDS, 1>(wt, src, rows, n, st0, st1, buf, lane, f);
+    else if (MAX_TG > 1 && n == 2)
+        pass_of<WORDS, 2>(wt, src, rows, n, st0, st1, buf, lane, f);
+    else if (MAX_TG > 1)
+        pass_of<WORDS, 4>(wt, src, rows, n, st0, st1, buf, lane, f);
+}
+
+template <int WORDS, int MAX_TG>
+constexpr int kWaveBuf = MAX_TG * kStepBlocks * 32 * kActDwords<WORDS>;
 
 // ------------------------------------------------------------------ gate and up
 
 // One workgroup: one expert and 32 consecutive h values (the quantization block
 // of the down projection's input).  Waves 0..3 take the gate rows, 4..7 the up
-// rows.
-template <int WORDS>
-__global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeArgs a) {
-    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS>];
-    __shared__ __align__(16) float gu[kTokenGroup][2][kHBlock];
+// rows; then a lane forms one h value, and the 32 lanes of a token quantize their
+// block as quantize4 does, value for value.  MAX_TG = 1: one token in the call.
+template <int WORDS, int MAX_TG>
+__global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_kernel(MoeArgs a) {
+    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS, MAX_TG>];
+    __shared__ __align__(16) float gu[MAX_TG][2][kHBlock];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nhb = a.nbf;
     const int act = static_cast<int>(blockIdx.x) / nhb, hb = static_cast<int>(blockIdx.x) % nhb;
     if (act >= a.plan->n_active) return;
     const MoeEntry en = a.plan->entry[act];
-    const int count = __popcll(en.mask);
+    const int count = MAX_TG == 1 ? 1 : __popcll(en.mask);
     const uint8_t *w = wave < 4 ? a.w_gate : a.w_up;
-    const WeightTile wt = weight_tile(w, static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave & 3) * kTileRows,
-                                      a.nbk, lane);
+    const __amdgpu_buffer_rsrc_t wt = weight_tile(w, static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave & 3) * kTileRows,
+                                                  a.nbk);
     const ActSource src = act_source<WORDS>(WORDS ? static_cast<const void *>(a.xq) : a.x, a.xs, a.rows, a.nbk);
     const int steps = (a.nbk + kStepBlocks - 1) / kStepBlocks;
-    const double post = WORDS == 2 ? 1.0 / 128.0 : 1.0;
-    for (int c0 = 0; c0 < count; c0 += kTokenGroup) {
-        int arow[kTokenGroup];
+    for (int c0 = 0; c0 < count; c0 += MAX_TG) {
+        const int n = min(MAX_TG, count - c0);
+        int rows[MAX_TG];
 #pragma unroll
-        for (int t = 0; t < kTokenGroup; ++t)
-            arow[t] = c0 + t < count ? a.plan->pair_token[en.offset + c0 + t] : -1;
-        double acc[kTokenGroup];
-#pragma unroll
-        for (int t = 0; t < kTokenGroup; ++t) acc[t] = 0.0;
-        run_steps<WORDS, kTokenGroup, 2>(wt, src, arow, 0, steps, bufs[wave], lane, acc);
-#pragma unroll
-        for (int t = 0; t < kTokenGroup; ++t) {
-            const double tot = row_sum(acc[t]) * post;
+        for (int t = 0; t < MAX_TG; ++t)
+            rows[t] = MAX_TG == 1 ? 0 : t < n ? a.plan->pair_token[en.offset + c0 + t] : -1;
+        pass<WORDS, MAX_TG>(wt, src, rows, n, 0, steps, bufs[wave], lane, [&](int t, double tot) {
             if ((lane & 7) == 0) gu[t][wave >> 2][(wave & 3) * kTileRows + (lane >> 3)] = static_cast<float>(tot);
-        }
+        });
         __syncthreads();
-        if (threadIdx.x < kTokenGroup * kQuantLanes) {
-            const int t = threadIdx.x / kQuantLanes, part = threadIdx.x % kQuantLanes;
-            float h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const double g = static_cast<double>(gu[t][0][part * 4 + i]);
-                const double u = static_cast<double>(gu[t][1][part * 4 + i]);
-                h[i] = static_cast<float>(g / (1.0 + exp(-g)) * u);
-            }
-            const float4 hv = make_float4(h[0], h[1], h[2], h[3]);
+        if (static_cast<int>(threadIdx.x) < n * kHBlock) {
+            const int t = threadIdx.x / kHBlock, i = threadIdx.x % kHBlock;
+            const double g = static_cast<double>(gu[t][0][i]), u = static_cast<double>(gu[t][1][i]);
+            const float h = static_cast<float>(g / (1.0 + exp(-g)) * u);
             const int64_t blk = static_cast<int64_t>(en.offset + c0 + t) * a.nbf + hb;
             if constexpr (WORDS == 0) {
-                if (c0 + t < count) reinterpret_cast<float4 *>(a.hq)[blk * kQuantLanes + part] = hv;
+                reinterpret_cast<float *>(a.hq)[blk * kHBlock + i] = h;
             } else {
-                uint32_t h4, l4;
-                const float s = quantize4<WORDS>(hv, h4, l4);
-                if (c0 + t < count) {
-                    uint32_t *rec = reinterpret_cast<uint32_t *>(a.hq + blk * (WORDS * 32));
-                    rec[part] = h4;
-                    if (WORDS == 2) rec[8 + part] = l4;
-                    if (part == 0) a.hs[blk] = s;
+                float amax = fabsf(h);
+#pragma unroll
+                for (int off = 1; off < kHBlock; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+                const float s = amax / 127.0f;
+                const int q = s == 0.0f ? 0 : quant_clamped(h / s);
+                int8_t *rec = reinterpret_cast<int8_t *>(a.hq) + blk * (WORDS * 32);
+                rec[i] = static_cast<int8_t>(q);
+                if constexpr (WORDS == 2) {
+                    const float rest = __builtin_fmaf(-s, static_cast<float>(q), h);
+                    rec[32 + i] = static_cast<int8_t>(s == 0.0f ? 0 : quant_clamped((rest * 128.0f) / s));
                 }
+                if (i == 0) a.hs[blk] = s;
             }
         }
-        __syncthreads();
+        if (c0 + MAX_TG < count) __syncthreads();
     }
 }
 
@@ -252,10 +307,10 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeArgs a) {
 // gate * (its part of a product) to its own f64 sums [rows][8], and the waves'
 // sums are added in wave order: the order of every sum depends on the choices
 // alone.
-template <int WORDS>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
+template <int WORDS, int MAX_TG>
+__global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_down_kernel(MoeArgs a) {
     extern __shared__ __align__(16) double sums[];  // [waves][rows][8]
-    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS>];
+    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS, MAX_TG>];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row0 = static_cast<int>(blockIdx.x) * kTileRows;
@@ -268,31 +323,22 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     const int from = static_cast<int>(static_cast<int64_t>(total) * wave / kWaves);
     const int to = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / kWaves);
     const ActSource src = act_source<WORDS>(a.hq, a.hs, a.rows * a.top_k, a.nbf);
-    const double post = WORDS == 2 ? 1.0 / 128.0 : 1.0;
     for (int at = from; at < to;) {
         const int act = at / steps, st0 = at - act * steps;
         const int st1 = min(steps, st0 + to - at);
         at += st1 - st0;
         const MoeEntry en = a.plan->entry[act];
-        const int count = __popcll(en.mask);
-        const WeightTile wt = weight_tile(a.w_down, static_cast<int64_t>(en.expert) * a.k + row0, a.nbf, lane);
-        for (int c0 = 0; c0 < count; c0 += kTokenGroup) {
-            int arow[kTokenGroup];
-            double acc[kTokenGroup];
+        const int count = MAX_TG == 1 ? 1 : __popcll(en.mask);
+        const __amdgpu_buffer_rsrc_t wt = weight_tile(a.w_down, static_cast<int64_t>(en.expert) * a.k + row0, a.nbf);
+        for (int c0 = 0; c0 < count; c0 += MAX_TG) {
+            const int first = en.offset + c0;
+            int rows[MAX_TG];
 #pragma unroll
-            for (int t = 0; t < kTokenGroup; ++t) {
-                arow[t] = c0 + t < count ? en.offset + c0 + t : -1;
-                acc[t] = 0.0;
-            }
-            run_steps<WORDS, kTokenGroup, 2>(wt, src, arow, st0, st1, bufs[wave], lane, acc);
-#pragma unroll
-            for (int t = 0; t < kTokenGroup; ++t) {
-                const double tot = row_sum(acc[t]) * post;
-                if (c0 + t < count && (lane & 7) == 0) {
-                    const int pair = en.offset + c0 + t;
-                    mine[a.plan->pair_token[pair] * kTileRows + (lane >> 3)] += a.plan->pair_gate[pair] * tot;
-                }
-            }
+            for (int t = 0; t < MAX_TG; ++t) rows[t] = first + t;
+            pass<WORDS, MAX_TG>(wt, src, rows, min(MAX_TG, count - c0), st0, st1, bufs[wave], lane, [&](int t, double tot) {
+                const int token = MAX_TG == 1 ? 0 : a.plan->pair_token[first + t];
+                if ((lane & 7) == 0) mine[token * kTileRows + (lane >> 3)] += a.plan->pair_gate[first + t] * tot;
+            });
         }
     }
     __syncthreads();
@@ -305,21 +351,26 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     }
 }
 
-template <int WORDS>
+template <int WORDS, int MAX_TG>
 hipError_t run(const MoeArgs &a, hipStream_t stream) {
     // at most one expert per (token, choice)
     const int most = std::min(a.experts, a.rows * a.top_k);
-    moe_gate_up_kernel<WORDS><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
+    moe_gate_up_kernel<WORDS, MAX_TG><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const size_t lds = static_cast<size_t>(kWaves) * a.rows * kTileRows * sizeof(double);
-    moe_down_kernel<WORDS><<<dim3(a.k / kTileRows), kThreads, lds, stream>>>(a);
+    moe_down_kernel<WORDS, MAX_TG><<<dim3(a.k / kTileRows), kThreads, lds, stream>>>(a);
     return hipGetLastError();
+}
+
+template <int MAX_TG>
+hipError_t run_mode(int mode, const MoeArgs &a, hipStream_t stream) {
+    return mode == 2 ? run<2, MAX_TG>(a, stream) : mode == 1 ? run<1, MAX_TG>(a, stream) : run<0, MAX_TG>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_moe_experts(int mode, const MoeArgs &a, hipStream_t stream) {
-    return mode == 2 ? run<2>(a, stream) : mode == 1 ? run<1>(a, stream) : run<0>(a, stream);
+    return a.rows == 1 ? run_mode<1>(mode, a, stream) : run_mode<kTokenGroup>(mode, a, stream);
 }
 
 }  // namespace q8

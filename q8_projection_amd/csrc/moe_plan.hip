@@ -13,42 +13,51 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTokenGroup = 8;  // tokens one wave dots a router row with
+constexpr int kTokenGroup = 8;  // tokens one workgroup dots a router row with
 
-// z[t][e] for one expert and up to 8 tokens: lanes stride over k four values at
-// a time, every product exact in f64 (24 x 24 bits) and every sum in f64.
-__device__ __forceinline__ void route_logits(const MoeArgs &a, int e, int t0, int lane) {
+// z[t][e] for one expert and up to 8 tokens, by one workgroup: threads stride over k
+// four values at a time (every product exact in f64, 24 x 24 bits, and every sum in
+// f64), the waves' sums are added in wave order.
+__device__ __forceinline__ void route_logits(const MoeArgs &a, int e, int t0) {
+    __shared__ double part[kWaves][kTokenGroup];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float4 *r = reinterpret_cast<const float4 *>(a.router + static_cast<int64_t>(e) * a.k);
     const int n4 = a.k / 4;
     const int nt = min(kTokenGroup, a.rows - t0);
+    const float4 *x = reinterpret_cast<const float4 *>(a.x + static_cast<int64_t>(t0) * a.k);
     double acc[kTokenGroup];
 #pragma unroll
     for (int t = 0; t < kTokenGroup; ++t) acc[t] = 0.0;
-    for (int i = lane; i < n4; i += 64) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n4; i += kThreads) {
         const float4 w = r[i];
 #pragma unroll
         for (int t = 0; t < kTokenGroup; ++t) {
             if (t >= nt) break;
-            const float4 x = reinterpret_cast<const float4 *>(a.x + static_cast<int64_t>(t0 + t) * a.k)[i];
-            acc[t] = __builtin_fma(static_cast<double>(w.x), static_cast<double>(x.x), acc[t]);
-            acc[t] = __builtin_fma(static_cast<double>(w.y), static_cast<double>(x.y), acc[t]);
-            acc[t] = __builtin_fma(static_cast<double>(w.z), static_cast<double>(x.z), acc[t]);
-            acc[t] = __builtin_fma(static_cast<double>(w.w), static_cast<double>(x.w), acc[t]);
+            const float4 v = x[static_cast<int64_t>(t) * n4 + i];
+            acc[t] = __builtin_fma(static_cast<double>(w.x), static_cast<double>(v.x), acc[t]);
+            acc[t] = __builtin_fma(static_cast<double>(w.y), static_cast<double>(v.y), acc[t]);
+            acc[t] = __builtin_fma(static_cast<double>(w.z), static_cast<double>(v.z), acc[t]);
+            acc[t] = __builtin_fma(static_cast<double>(w.w), static_cast<double>(v.w), acc[t]);
         }
     }
 #pragma unroll
     for (int t = 0; t < kTokenGroup; ++t) {
         if (t >= nt) break;
         const double z = wave_sum(acc[t]);
-        if (lane == 0) a.logits[static_cast<int64_t>(t0 + t) * a.experts + e] = static_cast<float>(z);
+        if (lane == 0) part[wave][t] = z;
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < nt) {
+        const double z = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+        a.logits[static_cast<int64_t>(t0 + t) * a.experts + e] = static_cast<float>(z);
     }
 }
 
 // Workgroups [0, quant_wgs) quantize x, the rest take router rows.
 template <int WORDS>
 __global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int quant_wgs) {
-    const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
     if constexpr (WORDS > 0) {
         if (static_cast<int>(blockIdx.x) < quant_wgs) {
             const int t = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
@@ -66,9 +75,8 @@ __global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int qu
             return;
         }
     }
-    const int item = (static_cast<int>(blockIdx.x) - quant_wgs) * kWaves + wave;
-    const int e = item % a.experts, g = item / a.experts;
-    if (g * kTokenGroup < a.rows) route_logits(a, e, g * kTokenGroup, lane);
+    const int item = static_cast<int>(blockIdx.x) - quant_wgs;
+    route_logits(a, item % a.experts, item / a.experts * kTokenGroup);
 }
 
 // The top_k largest logits of a token, in descending order, the lowest expert
@@ -88,28 +96,24 @@ __device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
     float mine = 0.f;       // lane i keeps choice i
     int mine_id = -1;
     uint32_t taken = 0;     // this lane's chosen j
+    const int nj = (a.experts + 63) / 64;
     for (int i = 0; i < a.top_k; ++i) {
         float bv = -__builtin_inff();
-        int be = INT32_MAX;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int e = lane + 64 * j;
-            const bool open = e < a.experts && !((taken >> j) & 1);
-            if (open && (v[j] > bv || (v[j] == bv && e < be))) {
-                bv = v[j];
-                be = e;
-            }
+            if (j >= nj) break;
+            if (!((taken >> j) & 1)) bv = fmaxf(bv, v[j]);
         }
+        bv = wave_max(bv);
+        // the lowest expert that has it
+        int be = -1;
 #pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const float ov = __shfl_xor(bv, off, 64);
-            const int oe = __shfl_xor(be, off, 64);
-            if (ov > bv || (ov == bv && oe < be)) {
-                bv = ov;
-                be = oe;
-            }
+        for (int j = 0; j < J; ++j) {
+            if (j >= nj || be >= 0) break;
+            const uint64_t has = __ballot(lane + 64 * j < a.experts && !((taken >> j) & 1) && v[j] == bv);
+            if (has) be = 64 * j + __builtin_ctzll(has);
         }
-        if (be == INT32_MAX) break;
+        if (be < 0) break;
         if ((be & 63) == lane) taken |= 1u << (be >> 6);
         if (i == 0) top = bv;
         sum += exp(static_cast<double>(bv) - static_cast<double>(top));
@@ -205,7 +209,7 @@ hipError_t launch_moe(int mode, const MoeArgs &a, bool route, bool experts, hipS
     const int quant_wgs =
         experts && mode != 0 ? (a.rows * a.nbk * kQuantLanes + kThreads - 1) / kThreads : 0;
     const int groups = (a.rows + kTokenGroup - 1) / kTokenGroup;
-    const int route_wgs = route ? (a.experts * groups + kWaves - 1) / kWaves : 0;
+    const int route_wgs = route ? a.experts * groups : 0;
     if (quant_wgs + route_wgs > 0) {
         const dim3 grid(quant_wgs + route_wgs);
         if (mode == 2)

@@ -55,25 +55,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float clean(float l) { return l == l ? l : -__builtin_inff(); }  // NaN: not a candidate
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-    return __uint_as_float(static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), CTRL, 0xf, 0xf, false)));
-}
-// Maximum over each 16 lanes.
-__device__ __forceinline__ float row_max(float v) {
-    v = fmaxf(v, dpp_f32<0xb1>(v));   // quad_perm [1,0,3,2]
-    v = fmaxf(v, dpp_f32<0x4e>(v));   // quad_perm [2,3,0,1]
-    v = fmaxf(v, dpp_f32<0x141>(v));  // row_half_mirror
-    return fmaxf(v, dpp_f32<0x140>(v));  // row_mirror
-}
-__device__ __forceinline__ float wave_max(float v) {
-    v = row_max(v);
-    const int b = static_cast<int>(__float_as_uint(v));
-    auto at = [&](int l) { return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(b, l))); };
-    return fmaxf(fmaxf(at(0), at(16)), fmaxf(at(32), at(48)));
-}
-
 // Up to four consecutive logits: those of [first, end) among row[at .. at + 3].  The
 // load is the same for every lane, with no branch around it (lanes at the end of the
 // row step back), so that several can be in flight; trim() makes the others -inf.
