@@ -1,4 +1,4 @@
-// moe_plan.hip -- the first steps of the mixture-of-experts layer: the router's
+// moe_plan.hip -- the first launch of the mixture-of-experts layer: the router's
 // logits, the activation quantization of x, the choice of experts and the plan
 // that groups the chosen (token, expert) pairs by expert.
 #include "actquant.h"
@@ -13,9 +13,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTokenGroup = 8;  // tokens one workgroup dots a router row with
+constexpr int kTokenGroup = 4;  // tokens one workgroup dots a router row with, and then a wave each chooses for
 
-// z[t][e] for one expert and up to 8 tokens, by one workgroup: threads stride over k
+// z[t][e] for one expert and up to 4 tokens, by one workgroup: threads stride over k
 // four values at a time (every product exact in f64, 24 x 24 bits, and every sum in
 // f64), the waves' sums are added in wave order.
 __device__ __forceinline__ void route_logits(const MoeArgs &a, int e, int t0) {
@@ -51,32 +51,9 @@ __device__ __forceinline__ void route_logits(const MoeArgs &a, int e, int t0) {
     const int t = threadIdx.x;
     if (t < nt) {
         const double z = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
-        a.logits[static_cast<int64_t>(t0 + t) * a.experts + e] = static_cast<float>(z);
+        __hip_atomic_store(a.logits + static_cast<int64_t>(t0 + t) * a.experts + e, static_cast<float>(z),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-}
-
-// Workgroups [0, quant_wgs) quantize x, the rest take router rows.
-template <int WORDS>
-__global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int quant_wgs) {
-    if constexpr (WORDS > 0) {
-        if (static_cast<int>(blockIdx.x) < quant_wgs) {
-            const int t = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
-            const int blk = t / kQuantLanes, part = t % kQuantLanes;
-            const bool valid = blk < a.rows * a.nbk;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid) v = reinterpret_cast<const float4 *>(a.x)[t];
-            uint32_t h4, l4;
-            const float s = quantize4<WORDS>(v, h4, l4);
-            if (!valid) return;
-            uint32_t *rec = reinterpret_cast<uint32_t *>(a.xq + static_cast<int64_t>(blk) * (WORDS * 32));
-            rec[part] = h4;
-            if (WORDS == 2) rec[8 + part] = l4;
-            if (part == 0) a.xs[blk] = s;
-            return;
-        }
-    }
-    const int item = static_cast<int>(blockIdx.x) - quant_wgs;
-    route_logits(a, item % a.experts, item / a.experts * kTokenGroup);
 }
 
 // The top_k largest logits of a token, in descending order, the lowest expert
@@ -89,13 +66,11 @@ __device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int e = lane + 64 * j;
-        v[j] = e < a.experts ? z[e] : -__builtin_inff();
+        v[j] = e < a.experts ? __hip_atomic_load(z + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -__builtin_inff();
     }
-    float top = 0.f;
-    double sum = 0.0;       // of the exps of the chosen, in order
-    float mine = 0.f;       // lane i keeps choice i
+    float mine = -__builtin_inff();  // lane i keeps choice i
     int mine_id = -1;
-    uint32_t taken = 0;     // this lane's chosen j
+    uint32_t taken = 0;              // this lane's chosen j
     const int nj = (a.experts + 63) / 64;
     for (int i = 0; i < a.top_k; ++i) {
         float bv = -__builtin_inff();
@@ -115,92 +90,172 @@ __device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
         }
         if (be < 0) break;
         if ((be & 63) == lane) taken |= 1u << (be >> 6);
-        if (i == 0) top = bv;
-        sum += exp(static_cast<double>(bv) - static_cast<double>(top));
         if (lane == i) {
             mine = bv;
             mine_id = be;
         }
     }
-    if (!a.renormalize) {
+    const double top = static_cast<double>(__builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), 0)));
+    const double mine_exp = mine_id < 0 ? 0.0 : exp(static_cast<double>(mine) - top);
+    double sum = 0.0;
+    if (a.renormalize) {
+        for (int i = 0; i < a.top_k; ++i) sum += readlane_f64(mine_exp, i);
+    } else {
         double s = 0.0;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-            if (lane + 64 * j < a.experts) s += exp(static_cast<double>(v[j]) - static_cast<double>(top));
+        for (int j = 0; j < J; ++j) {
+            if (j >= nj) break;
+            if (lane + 64 * j < a.experts) s += exp(static_cast<double>(v[j]) - top);
+        }
         sum = wave_sum(s);
     }
     if (lane < a.top_k) {
-        const double p = mine_id < 0 ? 0.0 : exp(static_cast<double>(mine) - static_cast<double>(top)) / sum;
-        a.ids[static_cast<int64_t>(t) * a.top_k + lane] = mine_id;
-        a.gates[static_cast<int64_t>(t) * a.top_k + lane] = static_cast<float>(p);
+        const double p = mine_id < 0 ? 0.0 : mine_exp / sum;
+        const int64_t at = static_cast<int64_t>(t) * a.top_k + lane;
+        __hip_atomic_store(a.ids + at, mine_id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.gates + at, static_cast<float>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
-constexpr int kPlanThreads = 1024;
-
-// One workgroup: the choices (route), then the plan (experts): per expert the
-// set of its tokens as a bit mask (or-ed, so the order of the threads does not
-// matter), the active experts in ascending order, and each pair's token and
-// gate at a place its mask gives.
-__global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(MoeArgs a, int route, int plan) {
+// The plan, by one workgroup: per expert the set of its tokens as a bit mask (or-ed,
+// so the order of the threads does not matter), the active experts in ascending
+// order, and each pair's token and gate at a place that its mask gives.
+__device__ __forceinline__ void make_plan(const MoeArgs &a) {
     __shared__ unsigned long long mask[kMoeMaxExperts];
-    __shared__ uint32_t scan[kMoeMaxExperts];
-    const int tid = threadIdx.x;
-    if (route) {
-        for (int t = tid >> 6; t < a.rows; t += kPlanThreads / 64) choose(a, t, tid & 63);
-        __threadfence_block();
-    }
-    if (!plan) return;
-    if (tid < kMoeMaxExperts) mask[tid] = 0;
-    __syncthreads();
+    __shared__ uint32_t before[kMoeMaxExperts];  // (active experts << 16 | pairs) before this one
+    __shared__ uint32_t wave_total[kWaves];
+    __shared__ int32_t ids[kMoeMaxPairs];
+    __shared__ float gates[kMoeMaxPairs];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int pairs = a.rows * a.top_k;
-    const int t = tid / a.top_k;
-    int id = -1;
-    if (tid < pairs) {
-        id = a.ids[tid];
-        if (id < 0 || id >= a.experts) id = -1;
-        if (id >= 0) atomicOr(&mask[id], 1ull << t);
+    constexpr int kPer = kMoeMaxPairs / kThreads;
+    int32_t id[kPer];
+    float gate[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // every load in flight at once
+        const int p = min(tid + i * kThreads, pairs - 1);
+        id[i] = __hip_atomic_load(a.ids + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        gate[i] = __hip_atomic_load(a.gates + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    for (int e = tid; e < a.experts; e += kThreads) mask[e] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int p = tid + i * kThreads;
+        if (p >= pairs) break;
+        const bool ok = id[i] >= 0 && id[i] < a.experts;
+        ids[p] = ok ? id[i] : -1;
+        gates[p] = gate[i];
+        if (ok) atomicOr(&mask[id[i]], 1ull << (p / a.top_k));
     }
     __syncthreads();
-    // inclusive scan of (active experts << 16 | pairs)
+    // each thread has consecutive experts; their totals are scanned over the workgroup
+    const int per = (a.experts + kThreads - 1) / kThreads;
     uint32_t own = 0;
-    if (tid < kMoeMaxExperts) {
-        const int c = __popcll(mask[tid]);
-        own = (c > 0 ? 1u << 16 : 0u) + static_cast<uint32_t>(c);
-        scan[tid] = own;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        const int c = e < a.experts ? __popcll(mask[e]) : 0;
+        own += (c > 0 ? 1u << 16 : 0u) + static_cast<uint32_t>(c);
     }
-    for (int off = 1; off < kMoeMaxExperts; off <<= 1) {
-        __syncthreads();
-        const uint32_t add = tid < kMoeMaxExperts && tid >= off ? scan[tid - off] : 0u;
-        __syncthreads();
-        if (tid < kMoeMaxExperts) scan[tid] += add;
+    uint32_t run = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(run, off, 64);
+        if (lane >= off) run += o;
+    }
+    if (lane == 63) wave_total[wave] = run;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) run += wave_total[w];
+    if (tid == kThreads - 1) a.plan->n_active = static_cast<int32_t>(run >> 16);
+    run -= own;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        const int c = e < a.experts ? __popcll(mask[e]) : 0;
+        if (c > 0) {
+            before[e] = run;
+            MoeEntry &en = a.plan->entry[run >> 16];
+            en.expert = e;
+            en.offset = static_cast<int32_t>(run & 0xffffu);
+            en.mask = mask[e];
+            run += (1u << 16) + static_cast<uint32_t>(c);
+        }
     }
     __syncthreads();
-    if (tid < kMoeMaxExperts && own) {
-        const uint32_t before = scan[tid] - own;
-        MoeEntry &en = a.plan->entry[before >> 16];
-        en.expert = tid;
-        en.offset = static_cast<int32_t>(before & 0xffffu);
-        en.mask = mask[tid];
-    }
-    if (tid == 0) a.plan->n_active = static_cast<int32_t>(scan[kMoeMaxExperts - 1] >> 16);
-    if (id >= 0) {
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = ids[p];
+        if (e < 0) continue;
         // a repeated choice counts once, with the sum of its gates in slot order
+        const int t = p / a.top_k;
         bool first = true;
-        double gate = 0.0;
-        for (int s = 0; s < a.top_k; ++s) {
-            const int p = t * a.top_k + s;
-            if (a.ids[p] != id) continue;
-            if (p < tid) first = false;
-            gate += static_cast<double>(a.gates[p]);
+        double sum = 0.0;
+        for (int q = t * a.top_k; q < (t + 1) * a.top_k; ++q) {
+            if (ids[q] != e) continue;
+            if (q < p) first = false;
+            sum += static_cast<double>(gates[q]);
         }
         if (first) {
-            const int c = __popcll(mask[id]);
-            const int at = static_cast<int>((scan[id] & 0xffffu)) - c + __popcll(mask[id] & ((1ull << t) - 1));
+            const int at = static_cast<int>(before[e] & 0xffffu) + __popcll(mask[e] & ((1ull << t) - 1));
             a.plan->pair_token[at] = t;
-            a.plan->pair_gate[at] = gate;
+            a.plan->pair_gate[at] = sum;
         }
     }
+}
+
+// Counts this workgroup in; true for the one that makes `total`, which puts the counter
+// back to zero.  What the workgroup has stored at agent scope is complete by then (the
+// waits), and the last one reads it at agent scope.
+__device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t total) {
+    __shared__ uint32_t done;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        done = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (done == total - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool last = done == total - 1;
+    __syncthreads();
+    return last;
+}
+
+// Workgroups [0, quant_wgs) quantize x.  The others take a router row and 4 tokens
+// each; the last of those tokens' workgroups makes their choices, and the last of all
+// makes the plan.  With given choices there is one more workgroup, for the plan.
+template <int WORDS>
+__global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int quant_wgs, int route, int plan) {
+    if constexpr (WORDS > 0) {
+        if (static_cast<int>(blockIdx.x) < quant_wgs) {
+            const int t = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+            const int blk = t / kQuantLanes, part = t % kQuantLanes;
+            const bool valid = blk < a.rows * a.nbk;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid) v = reinterpret_cast<const float4 *>(a.x)[t];
+            uint32_t h4, l4;
+            const float s = quantize4<WORDS>(v, h4, l4);
+            if (!valid) return;
+            uint32_t *rec = reinterpret_cast<uint32_t *>(a.xq + static_cast<int64_t>(blk) * (WORDS * 32));
+            rec[part] = h4;
+            if (WORDS == 2) rec[8 + part] = l4;
+            if (part == 0) a.xs[blk] = s;
+            return;
+        }
+    }
+    if (route) {
+        const int item = static_cast<int>(blockIdx.x) - quant_wgs;
+        const int group = item / a.experts, t0 = group * kTokenGroup;
+        route_logits(a, item - group * a.experts, t0);
+        if (!last_of(a.counters + group, static_cast<uint32_t>(a.experts))) return;
+        for (int t = t0 + (threadIdx.x >> 6); t < min(a.rows, t0 + kTokenGroup); t += kWaves) choose(a, t, threadIdx.x & 63);
+        const int groups = (a.rows + kTokenGroup - 1) / kTokenGroup;
+        if (!plan) return;
+        if (groups > 1) {
+            if (!last_of(a.counters + kMoeSlice / kTokenGroup, static_cast<uint32_t>(groups))) return;
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+        }
+    }
+    make_plan(a);
 }
 
 }  // namespace
@@ -209,18 +264,13 @@ hipError_t launch_moe(int mode, const MoeArgs &a, bool route, bool experts, hipS
     const int quant_wgs =
         experts && mode != 0 ? (a.rows * a.nbk * kQuantLanes + kThreads - 1) / kThreads : 0;
     const int groups = (a.rows + kTokenGroup - 1) / kTokenGroup;
-    const int route_wgs = route ? a.experts * groups : 0;
-    if (quant_wgs + route_wgs > 0) {
-        const dim3 grid(quant_wgs + route_wgs);
-        if (mode == 2)
-            moe_prepare_kernel<2><<<grid, kThreads, 0, stream>>>(a, quant_wgs);
-        else if (mode == 1)
-            moe_prepare_kernel<1><<<grid, kThreads, 0, stream>>>(a, quant_wgs);
-        else
-            moe_prepare_kernel<0><<<grid, kThreads, 0, stream>>>(a, quant_wgs);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    moe_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, route, experts);
+    const dim3 grid(quant_wgs + (route ? a.experts * groups : 1));
+    if (mode == 2)
+        moe_prepare_kernel<2><<<grid, kThreads, 0, stream>>>(a, quant_wgs, route, experts);
+    else if (mode == 1)
+        moe_prepare_kernel<1><<<grid, kThreads, 0, stream>>>(a, quant_wgs, route, experts);
+    else
+        moe_prepare_kernel<0><<<grid, kThreads, 0, stream>>>(a, quant_wgs, route, experts);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !experts) return e;
     return launch_moe_experts(mode, a, stream);
 }

@@ -26,6 +26,8 @@ class _MoeLayerC(ctypes.Structure):
 
 def _need(t, name: str, dtype, shape, device):
     """Raise ValueError unless t is a contiguous tensor of this dtype, shape and device."""
+    if type(t) is torch.Tensor and t.dtype == dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -38,34 +40,48 @@ def _need(t, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+_fns = {}
+
+
 def _call(fn: str, device, rows: int, stream, own, *args):
     """Call a library function on `device` and `stream` (None: its current
     stream).  `own`: tensors allocated here, which the caching allocator must
     not hand out again before the stream is done with them."""
+    if rows == 0:
+        return  # an empty tensor has no address; there is nothing to enqueue
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = _raw_stream(device.index)
     elif hasattr(stream, "cuda_stream"):
         raw = stream.cuda_stream
         for t in own:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(stream)
     else:
         raw = int(stream)
         if own:
             ext = torch.cuda.ExternalStream(raw, device=device)
             for t in own:
-                if t is not None:
-                    t.record_stream(ext)
-    if rows == 0:
-        return  # an empty tensor has no address; there is nothing to enqueue
-    f = getattr(_q8.lib(), fn)
-    if torch.cuda.current_device() == device.index:
+                t.record_stream(ext)
+    f = _fns.get(fn)
+    if f is None:
+        f = _fns[fn] = getattr(_q8.lib(), fn)
+    if _current_device() == device.index:
         status = f(*args, raw)
     else:
         with torch.cuda.device(device):
             status = f(*args, raw)
     if status != 0:
         raise _q8.Q8Error(fn, status)
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_current_device = torch.cuda.current_device
+# the same two answers without the wrappers around them, where torch has them (1-2 us a call)
+if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t):
