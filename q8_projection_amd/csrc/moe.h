@@ -55,7 +55,10 @@ struct MoeArgs {
     float *hs;              // [pairs][nbf]
 };
 
-constexpr int kMoeCounterBytes = 256;
+// Counters at the head of the workspace, a cache line each: workgroups that count in on
+// one line wait for each other (1024 of them on 16 neighbouring words took 12 us).
+constexpr int kMoeCounterStride = 32;  // words
+constexpr int kMoeCounterBytes = 32 * kMoeCounterStride * 4;
 
 inline int64_t moe_align(int64_t v) { return (v + 255) / 256 * 256; }
 

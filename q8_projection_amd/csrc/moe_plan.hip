@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+static_assert(kMoeCounterBytes / 4 / kMoeCounterStride > kMoeSlice / 4, "a counter for each token group and one more");
 constexpr int kTokenGroup = 4;  // tokens one workgroup dots a router row with, and then a wave each chooses for
 
 // z[t][e] for one expert and up to 4 tokens, by one workgroup: threads stride over k
@@ -58,63 +59,81 @@ __device__ __forceinline__ void route_logits(const MoeArgs &a, int e, int t0) {
 
 // The top_k largest logits of a token, in descending order, the lowest expert
 // among equals; one wave, experts dealt to lanes e = lane + 64 j.  A token whose
-// logits run out (NaN) gets id -1 and gate 0.
-__device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
-    constexpr int J = kMoeMaxExperts / 64;
+// logits run out (NaN) gets id -1 and gate 0.  Lane i returns choice i.
+template <int J>
+__device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane, int &id, float &gate) {
     const float *z = a.logits + static_cast<int64_t>(t) * a.experts;
     float v[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int e = lane + 64 * j;
-        v[j] = e < a.experts ? __hip_atomic_load(z + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -__builtin_inff();
+        v[j] = __hip_atomic_load(z + min(e, a.experts - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    float mine = -__builtin_inff();  // lane i keeps choice i
-    int mine_id = -1;
-    uint32_t taken = 0;              // this lane's chosen j
-    const int nj = (a.experts + 63) / 64;
+    uint32_t open = 0;  // this lane's j that are not chosen yet
+#pragma unroll
+    for (int j = 0; j < J; ++j) open |= lane + 64 * j < a.experts ? 1u << j : 0u;
+    const uint32_t all = open;
+    float mine = 0.f;
+    id = -1;
     for (int i = 0; i < a.top_k; ++i) {
         float bv = -__builtin_inff();
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (j >= nj) break;
-            if (!((taken >> j) & 1)) bv = fmaxf(bv, v[j]);
-        }
+        for (int j = 0; j < J; ++j) bv = fmaxf(bv, (open >> j) & 1 ? v[j] : -__builtin_inff());
         bv = wave_max(bv);
-        // the lowest expert that has it
-        int be = -1;
+        int be = -1;  // the lowest expert that has it
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (j >= nj || be >= 0) break;
-            const uint64_t has = __ballot(lane + 64 * j < a.experts && !((taken >> j) & 1) && v[j] == bv);
+        for (int j = J - 1; j >= 0; --j) {
+            const uint64_t has = __ballot(((open >> j) & 1) && v[j] == bv);
             if (has) be = 64 * j + __builtin_ctzll(has);
         }
         if (be < 0) break;
-        if ((be & 63) == lane) taken |= 1u << (be >> 6);
+        if ((be & 63) == lane) open &= ~(1u << (be >> 6));
         if (lane == i) {
             mine = bv;
-            mine_id = be;
+            id = be;
         }
     }
     const double top = static_cast<double>(__builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), 0)));
-    const double mine_exp = mine_id < 0 ? 0.0 : exp(static_cast<double>(mine) - top);
+    const double mine_exp = id < 0 ? 0.0 : exp(static_cast<double>(mine) - top);
     double sum = 0.0;
     if (a.renormalize) {
         for (int i = 0; i < a.top_k; ++i) sum += readlane_f64(mine_exp, i);
     } else {
-        double s = 0.0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (j >= nj) break;
-            if (lane + 64 * j < a.experts) s += exp(static_cast<double>(v[j]) - top);
-        }
-        sum = wave_sum(s);
+        for (int j = 0; j < J; ++j)
+            if ((all >> j) & 1) sum += exp(static_cast<double>(v[j]) - top);
+        sum = wave_sum(sum);
     }
-    if (lane < a.top_k) {
-        const double p = mine_id < 0 ? 0.0 : mine_exp / sum;
-        const int64_t at = static_cast<int64_t>(t) * a.top_k + lane;
-        __hip_atomic_store(a.ids + at, mine_id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(a.gates + at, static_cast<float>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    gate = static_cast<float>(id < 0 ? 0.0 : mine_exp / sum);
+}
+
+__device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane, int &id, float &gate) {
+    if (a.experts <= 64)
+        choose<1>(a, t, lane, id, gate);
+    else if (a.experts <= 128)
+        choose<2>(a, t, lane, id, gate);
+    else
+        choose<kMoeMaxExperts / 64>(a, t, lane, id, gate);
+}
+
+// The plan of a single token from its choices (all different, lane i has choice i):
+// its experts in ascending order.
+__device__ __forceinline__ void plan_one(const MoeArgs &a, int lane, int id, float gate) {
+    int before = 0, n = 0;
+    for (int i = 0; i < a.top_k; ++i) {
+        const int other = __builtin_amdgcn_readlane(id, i);
+        n += other >= 0;
+        before += other >= 0 && other < id;
     }
+    if (lane < a.top_k && id >= 0) {
+        MoeEntry &en = a.plan->entry[before];
+        en.expert = id;
+        en.offset = before;
+        en.mask = 1;
+        a.plan->pair_token[before] = 0;
+        a.plan->pair_gate[before] = static_cast<double>(gate);
+    }
+    if (lane == 0) a.plan->n_active = n;
 }
 
 // The plan, by one workgroup: per expert the set of its tokens as a bit mask (or-ed,
@@ -244,12 +263,25 @@ __global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int qu
         const int item = static_cast<int>(blockIdx.x) - quant_wgs;
         const int group = item / a.experts, t0 = group * kTokenGroup;
         route_logits(a, item - group * a.experts, t0);
-        if (!last_of(a.counters + group, static_cast<uint32_t>(a.experts))) return;
-        for (int t = t0 + (threadIdx.x >> 6); t < min(a.rows, t0 + kTokenGroup); t += kWaves) choose(a, t, threadIdx.x & 63);
+        if (!last_of(a.counters + group * kMoeCounterStride, static_cast<uint32_t>(a.experts))) return;
+        const int t = t0 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+        static_assert(kTokenGroup == kWaves, "a wave for each token");
+        if (t < a.rows) {
+            int id;
+            float gate;
+            choose(a, t, lane, id, gate);
+            if (lane < a.top_k) {
+                const int64_t at = static_cast<int64_t>(t) * a.top_k + lane;
+                __hip_atomic_store(a.ids + at, id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(a.gates + at, gate, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            if (plan && a.rows == 1) plan_one(a, lane, id, gate);
+        }
+        if (plan && a.rows == 1) return;
         const int groups = (a.rows + kTokenGroup - 1) / kTokenGroup;
         if (!plan) return;
         if (groups > 1) {
-            if (!last_of(a.counters + kMoeSlice / kTokenGroup, static_cast<uint32_t>(groups))) return;
+            if (!last_of(a.counters + kMoeSlice / kTokenGroup * kMoeCounterStride, static_cast<uint32_t>(groups))) return;
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();

@@ -170,7 +170,7 @@ def test_workspace_serves_layer_after_layer():
             got = q8.moe(layer, x, workspace=work)
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     torch.cuda.synchronize()
-    assert not work[:256].any()
+    assert not work[:4096].any()
 
 
 def test_replayed_graph_and_another_stream():
