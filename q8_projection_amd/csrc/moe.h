@@ -12,6 +12,15 @@ constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxPairs = kMoeSlice * kMoeMaxTopK;
 
+// Counters at the head of the workspace, a cache line each: workgroups that count in on
+// one line wait for each other (1024 of them on 16 neighbouring words took 12 us).
+constexpr int kMoeCounterStride = 32;  // words
+constexpr int kMoeMaxSplits = 8;
+constexpr int kMoeTileCounter = 32 * kMoeCounterStride;  // first of the down projection's counters, one a tile
+constexpr int kMoeMaxTiles = 512;                        // tiles whose work is split
+constexpr int kMoeCounterBytes = (kMoeTileCounter + kMoeMaxTiles) * 4;
+
+
 // One chosen expert: its tokens are the set bits of `mask` in ascending order,
 // and token number i of them is pair `offset + i`.
 struct MoeEntry {
@@ -45,20 +54,41 @@ struct MoeArgs {
     int renormalize;
     int k, nbk;
     int ff, nbf;
+    int tiled;              // quantized activations in the matrix-core order (below)
+    int sbk, sbf;           // blocks of one row of xq and hq: nbk and nbf, rounded up to four if tiled
+    int splits;             // workgroups that share a tile of the down projection
     // workspace
+    double *parts;          // [splits][k / 16][rows][16] partial outputs (splits > 1)
     uint32_t *counters;     // zero between calls
     MoePlan *plan;
     float *logits;          // [rows][experts]
-    uint8_t *xq;            // [rows][nbk][words * 32]: a block's hi words, then its lo words
-    float *xs;              // [rows][nbk]
-    uint8_t *hq;            // [pairs][nbf][words * 32] (f32 mode: f32 [pairs][ff])
-    float *hs;              // [pairs][nbf]
+    // Quantized rows.  Plain order: [row][block][word][32].  Tiled: [row][block / 4][word]
+    // [part 0..3][block % 4][8]: the four 8-byte parts that one lane of the matrix cores
+    // takes of four blocks are 32 bytes in a row; blocks that round a row up are zero.
+    uint8_t *xq;            // [rows][sbk] records of words * 32 bytes
+    float *xs;              // [rows][sbk]
+    uint8_t *hq;            // [pairs][sbf] records (f32 mode: f32 [pairs][ff])
+    float *hs;              // [pairs][sbf]
 };
 
-// Counters at the head of the workspace, a cache line each: workgroups that count in on
-// one line wait for each other (1024 of them on 16 neighbouring words took 12 us).
-constexpr int kMoeCounterStride = 32;  // words
-constexpr int kMoeCounterBytes = 32 * kMoeCounterStride * 4;
+// Byte offset of dword `part` (0..7) of block `blk`'s word in its row of records.
+__host__ __device__ inline int record_offset(int tiled, int words, int blk, int word, int part) {
+    return tiled ? (blk >> 2) * (words * 128) + word * 128 + (part >> 1) * 32 + (blk & 3) * 8 + (part & 1) * 4
+                 : blk * (words * 32) + word * 32 + part * 4;
+}
+
+// Whether the experts run on the matrix cores: integer modes, for a mean of more than
+// four tokens an expert.
+inline int moe_tiled(int words, const MoeArgs &a) { return words > 0 && a.rows * a.top_k > 4 * a.experts; }
+
+// Workgroups that share a tile of 16 output columns in the down projection on the
+// matrix cores: enough for two workgroups a CU.
+inline int moe_down_splits(const MoeArgs &a) {
+    if (!a.tiled) return 1;
+    int s = 1;
+    while (s < kMoeMaxSplits && a.k / 16 * s < 512) s *= 2;
+    return s;
+}
 
 inline int64_t moe_align(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -74,10 +104,15 @@ inline int64_t moe_layout(MoeArgs &a, uint8_t *base, int words) {
     a.counters = reinterpret_cast<uint32_t *>(take(kMoeCounterBytes));
     a.plan = reinterpret_cast<MoePlan *>(take(sizeof(MoePlan)));
     a.logits = reinterpret_cast<float *>(take(rows * a.experts * 4));
-    a.xq = take(rows * a.nbk * words * 32);
-    a.xs = reinterpret_cast<float *>(take(words ? rows * a.nbk * 4 : 0));
-    a.hq = take(words ? pairs * a.nbf * words * 32 : pairs * a.ff * 4);
-    a.hs = reinterpret_cast<float *>(take(words ? pairs * a.nbf * 4 : 0));
+    a.tiled = moe_tiled(words, a);
+    a.sbk = a.tiled ? (a.nbk + 3) / 4 * 4 : a.nbk;
+    a.sbf = a.tiled ? (a.nbf + 3) / 4 * 4 : a.nbf;
+    a.splits = moe_down_splits(a);
+    a.xq = take(rows * a.sbk * words * 32);
+    a.xs = reinterpret_cast<float *>(take(words ? rows * a.sbk * 4 : 0));
+    a.hq = take(words ? pairs * a.sbf * words * 32 : pairs * a.ff * 4);
+    a.hs = reinterpret_cast<float *>(take(words ? pairs * a.sbf * 4 : 0));
+    a.parts = reinterpret_cast<double *>(take(a.splits > 1 ? int64_t(8) * a.splits * rows * a.k : 0));
     return at;
 }
 

@@ -14,17 +14,25 @@ constexpr int kTileRows = 8;
 constexpr int kStepBlocks = 8;
 constexpr int kHBlock = 32;  // h values of one workgroup of the gate/up kernel: one quantization block
 constexpr uint32_t kBufferDword3 = 0x00020000u;
+constexpr uint32_t kOob = 0x80000000u;  // an offset past every range: loads there read zeros
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Dwords of activation words a lane carries per token and step: the step's 8
-// blocks of 32 values in 64 lanes.
+// Bytes of a record: one block's words (f32 mode: its 32 values).
 template <int WORDS>
-constexpr int kActDwords = WORDS == 0 ? 4 : WORDS;
+constexpr int kRec = WORDS == 0 ? 128 : 32 * WORDS;
+constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves, at most
+// Gate and up: two workgroups a CU; one in the f32 mode, whose conversions need the
+// registers.  (Down: one, measured against two, which spilled: 37 against 50 us.)
+template <int WORDS>
+constexpr int kWavesPerSimd = WORDS == 0 ? 2 : 4;
 
-// Activations of a launch: records of 32 values per block ([rows][nb] records
-// of 4 * 8 * kActDwords bytes) and block scales [rows][nb].
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), kBufferDword3);
+}
+
+// Activations of a launch: records [rows][nb] and block scales [rows][nb].
 struct ActSource {
     __amdgpu_buffer_rsrc_t words, scales;
     int nb;
@@ -32,118 +40,54 @@ struct ActSource {
 
 template <int WORDS>
 __device__ __forceinline__ ActSource act_source(const void *words, const float *scales, int rows, int nb) {
-    ActSource s;
-    s.words = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(words), 0, rows * nb * (32 * kActDwords<WORDS>),
-                                                kBufferDword3);
-    s.scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scales), 0, WORDS ? rows * nb * 4 : 0,
-                                                 kBufferDword3);
-    s.nb = nb;
-    return s;
+    return ActSource{buffer_of(words, rows * nb * kRec<WORDS>), buffer_of(scales, WORDS ? rows * nb * 4 : 0), nb};
 }
 
-// A tile of 8 rows of one expert's matrix, as a range-checked buffer.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_tile(const uint8_t *w, int64_t first_row, int nb) {
-    const uint32_t row_bytes = static_cast<uint32_t>(nb) * kBlockBytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(w + first_row * row_bytes), 0,
-                                             static_cast<int>(kTileRows * row_bytes), kBufferDword3);
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ float load_float(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
 
-template <int WORDS, int TG>
-struct Step {
-    Window w;
-    uint32_t a[TG][kActDwords<WORDS>];
-    float s[TG];
-};
+// The weights of a wave: a tile of 8 rows of one expert's matrix, step by step.  Lane
+// 8 r + s loads the window of block 8 step + s of row r; from `end` on (the row's last
+// block, the wave's last step) it reads zeros and touches no memory.
+struct Weights {
+    __amdgpu_buffer_rsrc_t tile;
+    uint32_t off;
+    int step, end;
 
-// Where a lane's loads of the next step are: its weight window (row lane / 8, block
-// lane % 8 of the step), its piece of each token's words (block lane / 8), and its
-// block's scales.  All move by a constant per step; from `w_end` and `a_end` on the
-// lane's blocks are behind the row's last or behind the wave's steps, and the loads
-// read zeros and touch no memory.
-template <int WORDS, int TG>
-struct Stream {
-    __amdgpu_buffer_rsrc_t tile, words, scales;
-    uint32_t w_off, a_off[TG], s_off[TG];
-    int step, w_end, a_end;
-
-    static constexpr int D = kActDwords<WORDS>;
-
-    __device__ __forceinline__ Stream(__amdgpu_buffer_rsrc_t weights, const ActSource &src, const int (&arow)[TG], int st0,
-                                      int st1, int lane) {
-        tile = weights;
-        words = src.words;
-        scales = src.scales;
+    __device__ __forceinline__ Weights(const uint8_t *w, int64_t first_row, int nb, int st0, int st1, int lane) {
+        const uint32_t row_bytes = static_cast<uint32_t>(nb) * kBlockBytes;
+        tile = buffer_of(w + first_row * row_bytes, kTileRows * row_bytes);
         step = st0;
-        // the first step at which 8 step + (lane's block) >= nb
-        w_end = min(st1, (src.nb - (lane & 7) + kStepBlocks - 1) / kStepBlocks);
-        a_end = min(st1, (src.nb - (lane >> 3) + kStepBlocks - 1) / kStepBlocks);
-        w_off = (lane >> 3) * static_cast<uint32_t>(src.nb) * kBlockBytes + st0 * (kStepBlocks * kBlockBytes) +
-                (((lane & 7) * kBlockBytes) & ~3u);
-#pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            const uint32_t block = static_cast<uint32_t>(arow[t]) * src.nb + st0 * kStepBlocks;
-            const uint32_t dead = oob_bit(arow[t] >= 0);
-            a_off[t] = ((block + (lane >> 3)) * (32 * D) + (lane & 7) * (4 * D)) | dead;
-            s_off[t] = ((block + (lane & 7)) * 4) | dead;
-        }
+        end = min(st1, (nb - (lane & 7) + kStepBlocks - 1) / kStepBlocks);
+        off = (lane >> 3) * row_bytes + st0 * (kStepBlocks * kBlockBytes) + (((lane & 7) * kBlockBytes) & ~3u);
     }
-
-    __device__ __forceinline__ void next(Step<WORDS, TG> &out) {
-        const uint32_t w_dead = oob_bit(step < w_end), a_dead = oob_bit(step < a_end);
-        const uint32_t off = w_off | w_dead;
-        const u32x4 d0 = __builtin_amdgcn_raw_buffer_load_b128(tile, off, 0, 0);
-        const u32x4 d1 = __builtin_amdgcn_raw_buffer_load_b128(tile, off + 16, 0, 0);
-        out.w.d[8] = __builtin_amdgcn_raw_buffer_load_b32(tile, off + 32, 0, 0);
-        out.w.d[0] = d0.x; out.w.d[1] = d0.y; out.w.d[2] = d0.z; out.w.d[3] = d0.w;
-        out.w.d[4] = d1.x; out.w.d[5] = d1.y; out.w.d[6] = d1.z; out.w.d[7] = d1.w;
-        w_off += kStepBlocks * kBlockBytes;
-#pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            const uint32_t ao = a_off[t] | a_dead;
-            if constexpr (D == 1) {
-                out.a[t][0] = __builtin_amdgcn_raw_buffer_load_b32(words, ao, 0, 0);
-            } else if constexpr (D == 2) {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(words, ao, 0, 0);
-                out.a[t][0] = v.x;
-                out.a[t][1] = v.y;
-            } else {
-                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(words, ao, 0, 0);
-                out.a[t][0] = v.x; out.a[t][1] = v.y; out.a[t][2] = v.z; out.a[t][3] = v.w;
-            }
-            a_off[t] += kStepBlocks * 32 * D;
-            if constexpr (WORDS > 0) {
-                out.s[t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales, s_off[t] | w_dead, 0, 0));
-                s_off[t] += kStepBlocks * 4;
-            }
-        }
+    __device__ __forceinline__ void next(Window &w) {
+        const uint32_t at = off | oob_bit(step < end);
+        const u32x4 d0 = __builtin_amdgcn_raw_buffer_load_b128(tile, at, 0, 0);
+        const u32x4 d1 = __builtin_amdgcn_raw_buffer_load_b128(tile, at + 16, 0, 0);
+        w.d[8] = __builtin_amdgcn_raw_buffer_load_b32(tile, at + 32, 0, 0);
+        w.d[0] = d0.x; w.d[1] = d0.y; w.d[2] = d0.z; w.d[3] = d0.w;
+        w.d[4] = d1.x; w.d[5] = d1.y; w.d[6] = d1.z; w.d[7] = d1.w;
+        off += kStepBlocks * kBlockBytes;
         ++step;
     }
 };
 
-// acc[t] += the step's block terms of the lane's row and block.
-template <int WORDS, int TG>
-__device__ __forceinline__ void compute(const Step<WORDS, TG> &st, uint8_t *buf, int lane, double (&acc)[TG]) {
-    constexpr int D = kActDwords<WORDS>;
-    constexpr int kRec = 32 * D;
-    wave_lds_sync();  // the previous step's reads come first
-#pragma unroll
-    for (int t = 0; t < TG; ++t) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>(buf + t * kStepBlocks * kRec) + lane * D;
-        if constexpr (D == 1)
-            dst[0] = st.a[t][0];
-        else if constexpr (D == 2)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(st.a[t][0], st.a[t][1]);
-        else
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(st.a[t][0], st.a[t][1], st.a[t][2], st.a[t][3]);
-    }
-    wave_lds_sync();
-    const int blk = lane & 7;
+// acc[t] += the block term of the lane's row and block with token t: the block's record
+// is at rec + t * REC_STRIDE and its scale at sc[t * SC_STRIDE] (the 8 rows of a wave
+// read the same addresses: broadcasts).
+template <int WORDS, int TG, int REC_STRIDE, int SC_STRIDE>
+__device__ __forceinline__ void compute(const Window &w, const uint8_t *rec, const float *sc, int lane, double (&acc)[TG]) {
     uint32_t q[8];
-    window_quants(st.w, window_selector(blk), q);
-    const double d = static_cast<double>(f16_bits_to_float(window_scale_bits(st.w, blk)));
+    window_quants(w, window_selector(lane & 7), q);
+    const double d = static_cast<double>(f16_bits_to_float(window_scale_bits(w, lane & 7)));
 #pragma unroll
-    for (int t = 0; t < TG; ++t) {
-        const uint8_t *rec = buf + (t * kStepBlocks + blk) * kRec;
+    for (int t = 0; t < TG; ++t, rec += REC_STRIDE) {
         if constexpr (WORDS == 0) {
             double p = 0.0;
 #pragma unroll
@@ -168,7 +112,7 @@ __device__ __forceinline__ void compute(const Step<WORDS, TG> &st, uint8_t *buf,
                 l[4] = l1.x; l[5] = l1.y; l[6] = l1.z; l[7] = l1.w;
                 tot = tot * 128 + dot32(q, l);
             }
-            acc[t] += (d * static_cast<double>(st.s[t])) * static_cast<double>(tot);
+            acc[t] += (d * static_cast<double>(sc[t * SC_STRIDE])) * static_cast<double>(tot);
         }
     }
 }
@@ -181,102 +125,124 @@ __device__ __forceinline__ double row_sum(double v) {
     return v;
 }
 
-// Steps [st0, st1) of one tile and TG tokens, P steps in flight.
-template <int WORDS, int TG, int P>
-__device__ __forceinline__ void run_steps(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int (&arow)[TG], int st0,
-                                          int st1, uint8_t *buf, int lane, double (&acc)[TG]) {
-    Stream<WORDS, TG> stream(wt, src, arow, st0, st1, lane);
-    Step<WORDS, TG> ring[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) stream.next(ring[p]);
-#pragma clang loop unroll(disable)
-    for (int s0 = st0; s0 < st1; s0 += P) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            compute<WORDS, TG>(ring[p], buf, lane, acc);
-            stream.next(ring[p]);
-            __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time in registers
-        }
-    }
-}
-
-constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves, at most
-
-// Steps in flight for a pass of TG tokens: as many loads ahead as registers allow at
-// two workgroups a CU.
-template <int TG>
-constexpr int kAhead = TG == 4 ? 2 : TG == 2 ? 3 : 4;
-// (one workgroup a CU in the f32 mode, whose conversions need the registers)
 template <int WORDS>
-constexpr int kWavesPerSimd = WORDS == 0 ? 2 : 4;
+constexpr double kPost = WORDS == 2 ? 1.0 / 128.0 : 1.0;
 
-// One pass over steps [st0, st1) of a tile for tokens rows[0 .. n) (n at most
-// kTokenGroup): f(token, total over the lanes of a row).
-template <int WORDS, int TG, typename F>
-__device__ __forceinline__ void pass_of(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int *rows, int n, int st0,
-                                        int st1, uint8_t *buf, int lane, F f) {
-    int arow[TG];
-    double acc[TG];
-#pragma unroll
-    for (int t = 0; t < TG; ++t) {
-        arow[t] = t < n ? rows[t] : -1;
-        acc[t] = 0.0;
-    }
-    run_steps<WORDS, TG, kAhead<TG>>(wt, src, arow, st0, st1, buf, lane, acc);
-#pragma unroll
-    for (int t = 0; t < TG; ++t)
-        if (t < n) f(t, row_sum(acc[t]) * (WORDS == 2 ? 1.0 / 128.0 : 1.0));
+// Hand LDS over between the waves of the workgroup; loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    workgroup_barrier_acquire_lds();
 }
-
-template <int WORDS, int MAX_TG, typename F>
-__device__ __forceinline__ void pass(__amdgpu_buffer_rsrc_t wt, const ActSource &src, const int *rows, int n, int st0,
-                                     int st1, uint8_t *buf, int lane, F f) {
-    if (MAX_TG == 1 || n == 1)
-        pass_of<WORDS, 1>(wt, src, rows, n, st0, st1, buf, lane, f);
-    else if (MAX_TG > 1 && n == 2)
-        pass_of<WORDS, 2>(wt, src, rows, n, st0, st1, buf, lane, f);
-    else if (MAX_TG > 1)
-        pass_of<WORDS, 4>(wt, src, rows, n, st0, st1, buf, lane, f);
-}
-
-template <int WORDS, int MAX_TG>
-constexpr int kWaveBuf = MAX_TG * kStepBlocks * 32 * kActDwords<WORDS>;
 
 // ------------------------------------------------------------------ gate and up
+
+// Blocks of the tokens' rows that are in LDS at a time, for all waves.
+template <int WORDS>
+constexpr int kChunk = WORDS == 0 ? 64 : 128;
+
+template <int WORDS, int MAX_TG>
+struct GateUpShared {
+    uint8_t words[MAX_TG][kChunk<WORDS> * kRec<WORDS>];
+    float scales[MAX_TG][kChunk<WORDS>];
+    float gu[MAX_TG][2][kHBlock];
+};
+
+// One pass: the wave's 8 rows of gate or up times n <= TG tokens, into s.gu.
+template <int WORDS, int TG, typename S>
+__device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t first_row, const ActSource &src,
+                                             const int *rows, int n, int lane, int wave) {
+    constexpr int C = kChunk<WORDS>, R = kRec<WORDS>;
+    constexpr int kAhead = WORDS == 0 ? 3 : TG == 4 ? 4 : 6;  // windows in flight
+    static_assert(C * R <= kThreads * 16 && C * TG <= kThreads, "a load a thread and token, a scale a thread");
+    const int tid = threadIdx.x;
+    double acc[TG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t) acc[t] = 0.0;
+    for (int b0 = 0; b0 < src.nb; b0 += C) {
+        const int nblk = min(C, src.nb - b0), steps = (nblk + kStepBlocks - 1) / kStepBlocks;
+        // the chunk's activations (zeros behind the row's last block), then the first
+        // windows: the loads come back in this order, so the wait for the activations
+        // leaves the windows in flight
+        uint4 v[TG];
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+            const bool ok = t < n && tid * 16 < nblk * R;
+            v[t] = load16(src.words, ok ? (static_cast<uint32_t>(rows[t]) * src.nb + b0) * R + tid * 16 : kOob);
+        }
+        float sc = 0.f;
+        if constexpr (WORDS > 0) {
+            const int t = tid / C, i = tid % C;
+            int row = rows[0];
+#pragma unroll
+            for (int u = 1; u < TG; ++u) row = t == u ? rows[u] : row;
+            sc = load_float(src.scales, t < n && i < nblk ? (static_cast<uint32_t>(row) * src.nb + b0 + i) * 4 : kOob);
+        }
+        Weights wt(w, first_row, src.nb, b0 / kStepBlocks, b0 / kStepBlocks + steps, lane);
+        Window ring[kAhead];
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) wt.next(ring[p]);
+        if (b0 > 0) lds_barrier();  // the last chunk has been read
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+            if (tid * 16 < C * R) *reinterpret_cast<uint4 *>(s.words[t] + tid * 16) = v[t];
+        if constexpr (WORDS > 0)
+            if (tid < C * TG) s.scales[tid / C][tid % C] = sc;
+        lds_barrier();
+        const uint8_t *rec = s.words[0] + (lane & 7) * R;
+        const float *scale = s.scales[0] + (lane & 7);
+#pragma clang loop unroll(disable)
+        for (int s0 = 0; s0 < steps; s0 += kAhead) {
+#pragma unroll
+            for (int p = 0; p < kAhead; ++p) {
+                // a dead step's windows are zeros; its activations are read from the chunk
+                const int at = min(s0 + p, C / kStepBlocks - 1);
+                compute<WORDS, TG, C * R, C>(ring[p], rec + at * (kStepBlocks * R), scale + at * kStepBlocks, lane, acc);
+                wt.next(ring[p]);
+                __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time in registers
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+        const double tot = row_sum(acc[t]) * kPost<WORDS>;
+        if (t < n && (lane & 7) == 0) s.gu[t][wave >> 2][(wave & 3) * kTileRows + (lane >> 3)] = static_cast<float>(tot);
+    }
+}
 
 // One workgroup: one expert and 32 consecutive h values (the quantization block
 // of the down projection's input).  Waves 0..3 take the gate rows, 4..7 the up
 // rows; then a lane forms one h value, and the 32 lanes of a token quantize their
-// block as quantize4 does, value for value.  MAX_TG = 1: one token in the call.
-template <int WORDS, int MAX_TG>
+// block as quantize4 does, value for value.  MAX_TG: tokens a pass takes, at most;
+// ONE: one token in the call.
+template <int WORDS, int MAX_TG, bool ONE>
 __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_kernel(MoeArgs a) {
-    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS, MAX_TG>];
-    __shared__ __align__(16) float gu[MAX_TG][2][kHBlock];
+    __shared__ __align__(16) GateUpShared<WORDS, MAX_TG> s;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nhb = a.nbf;
     const int act = static_cast<int>(blockIdx.x) / nhb, hb = static_cast<int>(blockIdx.x) % nhb;
     if (act >= a.plan->n_active) return;
     const MoeEntry en = a.plan->entry[act];
-    const int count = MAX_TG == 1 ? 1 : __popcll(en.mask);
+    const int count = ONE ? 1 : __popcll(en.mask);
     const uint8_t *w = wave < 4 ? a.w_gate : a.w_up;
-    const __amdgpu_buffer_rsrc_t wt = weight_tile(w, static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave & 3) * kTileRows,
-                                                  a.nbk);
+    const int64_t first_row = static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave & 3) * kTileRows;
     const ActSource src = act_source<WORDS>(WORDS ? static_cast<const void *>(a.xq) : a.x, a.xs, a.rows, a.nbk);
-    const int steps = (a.nbk + kStepBlocks - 1) / kStepBlocks;
     for (int c0 = 0; c0 < count; c0 += MAX_TG) {
         const int n = min(MAX_TG, count - c0);
         int rows[MAX_TG];
 #pragma unroll
         for (int t = 0; t < MAX_TG; ++t)
-            rows[t] = MAX_TG == 1 ? 0 : t < n ? a.plan->pair_token[en.offset + c0 + t] : -1;
-        pass<WORDS, MAX_TG>(wt, src, rows, n, 0, steps, bufs[wave], lane, [&](int t, double tot) {
-            if ((lane & 7) == 0) gu[t][wave >> 2][(wave & 3) * kTileRows + (lane >> 3)] = static_cast<float>(tot);
-        });
+            rows[t] = ONE ? 0 : __builtin_amdgcn_readfirstlane(a.plan->pair_token[en.offset + c0 + min(t, n - 1)]);
+        if (MAX_TG == 1 || n == 1)
+            gate_up_pass<WORDS, 1>(s, w, first_row, src, rows, n, lane, wave);
+        else if (MAX_TG > 1 && n == 2)
+            gate_up_pass<WORDS, MAX_TG == 1 ? 1 : 2>(s, w, first_row, src, rows, n, lane, wave);
+        else
+            gate_up_pass<WORDS, MAX_TG>(s, w, first_row, src, rows, n, lane, wave);
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < n * kHBlock) {
             const int t = threadIdx.x / kHBlock, i = threadIdx.x % kHBlock;
-            const double g = static_cast<double>(gu[t][0][i]), u = static_cast<double>(gu[t][1][i]);
+            const double g = static_cast<double>(s.gu[t][0][i]), u = static_cast<double>(s.gu[t][1][i]);
             const float h = static_cast<float>(g / (1.0 + exp(-g)) * u);
             const int64_t blk = static_cast<int64_t>(en.offset + c0 + t) * a.nbf + hb;
             if constexpr (WORDS == 0) {
@@ -285,15 +251,15 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_ke
                 float amax = fabsf(h);
 #pragma unroll
                 for (int off = 1; off < kHBlock; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-                const float s = amax / 127.0f;
-                const int q = s == 0.0f ? 0 : quant_clamped(h / s);
+                const float sc = amax / 127.0f;
+                const int q = sc == 0.0f ? 0 : quant_clamped(h / sc);
                 int8_t *rec = reinterpret_cast<int8_t *>(a.hq) + blk * (WORDS * 32);
                 rec[i] = static_cast<int8_t>(q);
                 if constexpr (WORDS == 2) {
-                    const float rest = __builtin_fmaf(-s, static_cast<float>(q), h);
-                    rec[32 + i] = static_cast<int8_t>(s == 0.0f ? 0 : quant_clamped((rest * 128.0f) / s));
+                    const float rest = __builtin_fmaf(-sc, static_cast<float>(q), h);
+                    rec[32 + i] = static_cast<int8_t>(sc == 0.0f ? 0 : quant_clamped((rest * 128.0f) / sc));
                 }
-                if (i == 0) a.hs[blk] = s;
+                if (i == 0) a.hs[blk] = sc;
             }
         }
         if (c0 + MAX_TG < count) __syncthreads();
@@ -302,15 +268,91 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_ke
 
 // ------------------------------------------------------------------------- down
 
+// Steps of a pass whose activations a wave has in LDS at a time.
+template <int TG>
+constexpr int kSeg = TG == 4 ? 2 : 4;
+template <int WORDS, int MAX_TG>
+constexpr int kWaveBytes = MAX_TG * kSeg<MAX_TG> * kStepBlocks * kRec<WORDS>;
+
+// One pass over steps [st0, st1) of the wave's tile for the tokens (pairs) first ..
+// first + n - 1: f(token number, total of the lane's row).  The activations of kSeg
+// steps at a time go through the wave's own piece of LDS, loaded a segment ahead as
+// whole kilobytes: the loads of small pieces (one for each step and token) had cost
+// more than the weights' at four tokens.
+template <int WORDS, int TG, typename F>
+__device__ __forceinline__ void down_pass(uint8_t *buf, float *sbuf, const uint8_t *w, int64_t first_row,
+                                          const ActSource &src, int first, int n, int st0, int st1, int lane, F f) {
+    constexpr int S = kSeg<TG>, R = kRec<WORDS>;
+    constexpr int kSegBlocks = S * kStepBlocks, kSegBytes = kSegBlocks * R;
+    constexpr int kLoads = (kSegBytes + 1023) / 1024;  // of 1 KB, per token and segment
+    constexpr int kAhead = TG == 4 ? 2 : 4;            // windows in flight
+    static_assert(TG * kSegBlocks <= 64, "a scale a lane");
+    double acc[TG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t) acc[t] = 0.0;
+    uint4 v[TG][kLoads];
+    float sc = 0.f;
+    auto load = [&](int st) {  // the segment that begins at step st
+        const int b0 = st * kStepBlocks;
+        const int nblk = st < st1 ? min(kSegBlocks, src.nb - b0) : 0;
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int at = k * 1024 + lane * 16;
+                const bool ok = t < n && at < nblk * R;
+                v[t][k] = load16(src.words, ok ? (static_cast<uint32_t>(first + t) * src.nb + b0) * R + at : kOob);
+            }
+        if constexpr (WORDS > 0) {
+            const int t = lane / kSegBlocks, i = lane % kSegBlocks;
+            sc = load_float(src.scales, t < n && i < nblk ? (static_cast<uint32_t>(first + t) * src.nb + b0 + i) * 4 : kOob);
+        }
+    };
+    load(st0);
+    Weights wt(w, first_row, src.nb, st0, st1, lane);
+    Window ring[kAhead];
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) wt.next(ring[p]);
+    const uint8_t *rec = buf + (lane & 7) * R;
+    const float *scale = sbuf + (lane & 7);
+#pragma clang loop unroll(disable)
+    for (int s0 = st0; s0 < st1; s0 += kAhead) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+            if (p % S == 0) {
+                wave_lds_sync();  // the last segment has been read
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+                        if (kSegBytes >= 1024 || lane * 16 < kSegBytes)
+                            *reinterpret_cast<uint4 *>(buf + t * kSegBytes + k * 1024 + lane * 16) = v[t][k];
+                if constexpr (WORDS > 0)
+                    if (lane < TG * kSegBlocks) sbuf[lane] = sc;
+                wave_lds_sync();
+                load(s0 + p + S);
+            }
+            compute<WORDS, TG, kSegBytes, kSegBlocks>(ring[p], rec + (p % S) * (kStepBlocks * R), scale + (p % S) * kStepBlocks,
+                                                      lane, acc);
+            wt.next(ring[p]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+        if (t < n) f(t, row_sum(acc[t]) * kPost<WORDS>);
+}
+
 // One workgroup: 8 output columns of y for every token.  The chosen experts'
 // steps, laid end to end, are split evenly over the 8 waves; a wave adds
 // gate * (its part of a product) to its own f64 sums [rows][8], and the waves'
 // sums are added in wave order: the order of every sum depends on the choices
 // alone.
-template <int WORDS, int MAX_TG>
-__global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_down_kernel(MoeArgs a) {
+template <int WORDS, int MAX_TG, bool ONE>
+__global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeArgs a) {
     extern __shared__ __align__(16) double sums[];  // [waves][rows][8]
-    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBuf<WORDS, MAX_TG>];
+    __shared__ __align__(16) uint8_t bufs[kWaves][kWaveBytes<WORDS, MAX_TG>];
+    __shared__ float sbufs[kWaves][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row0 = static_cast<int>(blockIdx.x) * kTileRows;
@@ -328,17 +370,20 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_down_kerne
         const int st1 = min(steps, st0 + to - at);
         at += st1 - st0;
         const MoeEntry en = a.plan->entry[act];
-        const int count = MAX_TG == 1 ? 1 : __popcll(en.mask);
-        const __amdgpu_buffer_rsrc_t wt = weight_tile(a.w_down, static_cast<int64_t>(en.expert) * a.k + row0, a.nbf);
+        const int count = ONE ? 1 : __popcll(en.mask);
+        const int64_t first_row = static_cast<int64_t>(en.expert) * a.k + row0;
         for (int c0 = 0; c0 < count; c0 += MAX_TG) {
-            const int first = en.offset + c0;
-            int rows[MAX_TG];
-#pragma unroll
-            for (int t = 0; t < MAX_TG; ++t) rows[t] = first + t;
-            pass<WORDS, MAX_TG>(wt, src, rows, min(MAX_TG, count - c0), st0, st1, bufs[wave], lane, [&](int t, double tot) {
-                const int token = MAX_TG == 1 ? 0 : a.plan->pair_token[first + t];
+            const int first = en.offset + c0, n = min(MAX_TG, count - c0);
+            const auto add = [&](int t, double tot) {
+                const int token = ONE ? 0 : a.plan->pair_token[first + t];
                 if ((lane & 7) == 0) mine[token * kTileRows + (lane >> 3)] += a.plan->pair_gate[first + t] * tot;
-            });
+            };
+            if (MAX_TG == 1 || n == 1)
+                down_pass<WORDS, 1>(bufs[wave], sbufs[wave], a.w_down, first_row, src, first, n, st0, st1, lane, add);
+            else if (MAX_TG > 1 && n == 2)
+                down_pass<WORDS, MAX_TG == 1 ? 1 : 2>(bufs[wave], sbufs[wave], a.w_down, first_row, src, first, n, st0, st1, lane, add);
+            else
+                down_pass<WORDS, MAX_TG>(bufs[wave], sbufs[wave], a.w_down, first_row, src, first, n, st0, st1, lane, add);
         }
     }
     __syncthreads();
@@ -351,26 +396,28 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_down_kerne
     }
 }
 
-template <int WORDS, int MAX_TG>
+template <int WORDS, int MAX_TG, bool ONE = false>
 hipError_t run(const MoeArgs &a, hipStream_t stream) {
     // at most one expert per (token, choice)
     const int most = std::min(a.experts, a.rows * a.top_k);
-    moe_gate_up_kernel<WORDS, MAX_TG><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
+    moe_gate_up_kernel<WORDS, MAX_TG, ONE><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const size_t lds = static_cast<size_t>(kWaves) * a.rows * kTileRows * sizeof(double);
-    moe_down_kernel<WORDS, MAX_TG><<<dim3(a.k / kTileRows), kThreads, lds, stream>>>(a);
+    moe_down_kernel<WORDS, MAX_TG, ONE><<<dim3(a.k / kTileRows), kThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
-template <int MAX_TG>
-hipError_t run_mode(int mode, const MoeArgs &a, hipStream_t stream) {
-    return mode == 2 ? run<2, MAX_TG>(a, stream) : mode == 1 ? run<1, MAX_TG>(a, stream) : run<0, MAX_TG>(a, stream);
+template <int WORDS>
+hipError_t run_words(const MoeArgs &a, hipStream_t stream) {
+    if (a.rows == 1) return run<WORDS, 1, true>(a, stream);
+    return run<WORDS, kTokenGroup>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_moe_experts(int mode, const MoeArgs &a, hipStream_t stream) {
-    return a.rows == 1 ? run_mode<1>(mode, a, stream) : run_mode<kTokenGroup>(mode, a, stream);
+    if (a.tiled) return launch_moe_mma(mode, a, stream);
+    return mode == 2 ? run_words<2>(a, stream) : mode == 1 ? run_words<1>(a, stream) : run_words<0>(a, stream);
 }
 
 }  // namespace q8

@@ -20,5 +20,7 @@
 namespace q8 {
 
 hipError_t launch_moe_experts(int mode, const MoeArgs &a, hipStream_t stream);
+// The same on the int8 matrix cores (integer modes, tiled activations): moe_mma.hip.
+hipError_t launch_moe_mma(int mode, const MoeArgs &a, hipStream_t stream);
 
 }  // namespace q8

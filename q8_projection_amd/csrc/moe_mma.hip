@@ -1,0 +1,441 @@
+// moe_mma.hip -- the chosen experts' projections on the int8 matrix cores, for
+// integer stacks of two and more rows.
+//
+// Tiles.  v_mfma_i32_16x16x32_i8 takes one Q8_0 block of 16 weight rows against 16
+// activation columns: lane l supplies bytes 8 q .. 8 q + 7 (q = l / 16) of row, or
+// column, l % 16, and receives the exact sums of weight row l % 16 with columns
+// 4 q .. 4 q + 3.  The columns are the tokens of one expert: 16 in the one-word mode,
+// 8 (hi and lo words side by side) in the two-word mode.
+//
+// Weights go from memory to registers without LDS: lane (r, q) loads the window of
+// block 4 s + q of row r, so that a step of the wave is 136 contiguous bytes of each
+// of 16 rows, and a 4 x 4 exchange of 8-byte parts between the lanes of a row (eight
+// swaps of half and quarter waves) turns four whole blocks in four lanes into four
+// operands in every lane.  The activations are stored in the operands' order, and a
+// lane reads its four parts as 32 contiguous bytes.
+//
+// Sums.  Every block term (d s) T is added in f64, as everywhere in this library.
+#include <algorithm>
+
+#include "moe_kernels.h"
+
+#pragma clang fp contract(off)
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kTileRows = 16;
+constexpr int kStepBlocks = 4;
+constexpr int kHBlock = 32;  // h values of one workgroup of the gate/up kernel: one quantization block
+constexpr uint32_t kBufferDword3 = 0x00020000u;
+constexpr uint32_t kOob = 0x80000000u;  // an offset past every range: loads there read zeros
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+template <int WORDS>
+struct Tile {
+    static constexpr int kTokens = 16 / WORDS;  // tokens of a tile's 16 columns
+    static constexpr int kVals = kTokens / 4;   // results a lane has of them
+    // column m: one word of one token; lane q's four columns are its kVals tokens' words
+    static __device__ __forceinline__ int token(int m) { return WORDS == 2 ? m >> 1 : m; }
+    static __device__ __forceinline__ int word(int m) { return WORDS == 2 ? m & 1 : 0; }
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), kBufferDword3);
+}
+
+// 16 rows of one expert's matrix (fewer at its end: `rows`).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_tile(const uint8_t *w, int64_t first_row, int nb) {
+    const uint32_t row_bytes = static_cast<uint32_t>(nb) * kBlockBytes;
+    return buffer_of(w + first_row * row_bytes, kTileRows * row_bytes);
+}
+
+// The window of the lane's block (row lane % 16, block 4 step + lane / 16); zeros for
+// blocks behind the row's last and for steps that are not the wave's.
+__device__ __forceinline__ void load_weights(__amdgpu_buffer_rsrc_t tile, uint32_t lane_off, int step, bool live,
+                                             Window &w) {
+    const uint32_t off = (lane_off + step * (kStepBlocks * kBlockBytes)) | oob_bit(live);
+    const u32x4 d0 = __builtin_amdgcn_raw_buffer_load_b128(tile, off, 0, 0);
+    const u32x4 d1 = __builtin_amdgcn_raw_buffer_load_b128(tile, off + 16, 0, 0);
+    w.d[8] = __builtin_amdgcn_raw_buffer_load_b32(tile, off + 32, 0, 0);
+    w.d[0] = d0.x; w.d[1] = d0.y; w.d[2] = d0.z; w.d[3] = d0.w;
+    w.d[4] = d1.x; w.d[5] = d1.y; w.d[6] = d1.z; w.d[7] = d1.w;
+}
+
+// The activations of one token tile: the lane's operand parts of four blocks, and the
+// block scales of its kVals tokens.
+template <int WORDS>
+struct Acts {
+    long part[kStepBlocks];
+    float s[Tile<WORDS>::kVals][kStepBlocks];
+};
+
+// Offsets of a lane's loads (of step 0), kOob where it has no token.
+template <int WORDS>
+struct ActOffsets {
+    uint32_t part, s[Tile<WORDS>::kVals];
+};
+
+// `row(i)`: row of xq or hq of the tile's token i, or -1.
+template <int WORDS, typename F>
+__device__ __forceinline__ ActOffsets<WORDS> act_offsets(int sb, int lane, F row) {
+    const int m = lane & 15, q = lane >> 4;
+    ActOffsets<WORDS> o;
+    const int mine = row(Tile<WORDS>::token(m));
+    o.part = mine >= 0 ? static_cast<uint32_t>(mine) * sb * (WORDS * 32) + Tile<WORDS>::word(m) * 128 + q * 32 : kOob;
+#pragma unroll
+    for (int v = 0; v < Tile<WORDS>::kVals; ++v) {
+        const int r = row(q * Tile<WORDS>::kVals + v);
+        o.s[v] = r >= 0 ? static_cast<uint32_t>(r) * sb * 4 : kOob;
+    }
+    return o;
+}
+
+template <int WORDS>
+__device__ __forceinline__ void load_acts(__amdgpu_buffer_rsrc_t words, __amdgpu_buffer_rsrc_t scales,
+                                          const ActOffsets<WORDS> &o, int step, bool live, Acts<WORDS> &a) {
+    const uint32_t dead = oob_bit(live), off = (o.part + step * (WORDS * 128)) | dead;
+    const u32x4 p0 = __builtin_amdgcn_raw_buffer_load_b128(words, off, 0, 0);
+    const u32x4 p1 = __builtin_amdgcn_raw_buffer_load_b128(words, off + 16, 0, 0);
+    a.part[0] = static_cast<long>((static_cast<uint64_t>(p0.y) << 32) | p0.x);
+    a.part[1] = static_cast<long>((static_cast<uint64_t>(p0.w) << 32) | p0.z);
+    a.part[2] = static_cast<long>((static_cast<uint64_t>(p1.y) << 32) | p1.x);
+    a.part[3] = static_cast<long>((static_cast<uint64_t>(p1.w) << 32) | p1.z);
+#pragma unroll
+    for (int v = 0; v < Tile<WORDS>::kVals; ++v) {
+        const u32x4 s = __builtin_amdgcn_raw_buffer_load_b128(scales, (o.s[v] + step * 16) | dead, 0, 0);
+        a.s[v][0] = __uint_as_float(s.x); a.s[v][1] = __uint_as_float(s.y);
+        a.s[v][2] = __uint_as_float(s.z); a.s[v][3] = __uint_as_float(s.w);
+    }
+}
+
+// (a, b) of lanes (q 0,1 | q 2,3): the upper half of a changes places with the lower half of b.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r.x;
+    b = r.y;
+}
+// The odd rows of 16 lanes of a change places with the even rows of b.
+__device__ __forceinline__ void swap_rows(uint32_t &a, uint32_t &b) {
+    const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r.x;
+    b = r.y;
+}
+
+// The matrix-core operands and scales of four blocks of a lane's row.
+struct Operands {
+    long part[kStepBlocks];
+    double d[kStepBlocks];
+};
+
+__device__ __forceinline__ void operands_of(const Window &w, int lane, Operands &o) {
+    const int q = lane >> 4;  // the parity of the lane's block
+    uint32_t e[8];
+    window_quants(w, window_selector(q), e);
+    // e[2p], e[2p + 1]: part p of block q.  Afterwards part q of block j is in e[2j], e[2j + 1].
+    swap_halves(e[0], e[4]);
+    swap_halves(e[1], e[5]);
+    swap_halves(e[2], e[6]);
+    swap_halves(e[3], e[7]);
+    swap_rows(e[0], e[2]);
+    swap_rows(e[1], e[3]);
+    swap_rows(e[4], e[6]);
+    swap_rows(e[5], e[7]);
+#pragma unroll
+    for (int j = 0; j < kStepBlocks; ++j)
+        o.part[j] = static_cast<long>((static_cast<uint64_t>(e[2 * j + 1]) << 32) | e[2 * j]);
+    // the four blocks' scales to all four lanes
+    uint32_t d0 = __float_as_uint(f16_bits_to_float(window_scale_bits(w, q))), d2 = d0;
+    swap_halves(d0, d2);
+    uint32_t d1 = d0, d3 = d2;
+    swap_rows(d0, d1);
+    swap_rows(d2, d3);
+    o.d[0] = static_cast<double>(__uint_as_float(d0));
+    o.d[1] = static_cast<double>(__uint_as_float(d1));
+    o.d[2] = static_cast<double>(__uint_as_float(d2));
+    o.d[3] = static_cast<double>(__uint_as_float(d3));
+}
+
+// acc[v] += the four block terms of the lane's row with its tokens.
+template <int WORDS>
+__device__ __forceinline__ void multiply(const Operands &w, const Acts<WORDS> &a, double (&acc)[Tile<WORDS>::kVals]) {
+#pragma unroll
+    for (int j = 0; j < kStepBlocks; ++j) {
+        const v4i sum = __builtin_amdgcn_mfma_i32_16x16x32_i8(a.part[j], w.part[j], v4i{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < Tile<WORDS>::kVals; ++v) {
+            const int t = WORDS == 2 ? sum[2 * v] * 128 + sum[2 * v + 1] : sum[v];
+            acc[v] = __builtin_fma(w.d[j] * static_cast<double>(a.s[v][j]), static_cast<double>(t), acc[v]);
+        }
+    }
+}
+
+// Two workgroups a CU where the registers of one token tile allow it, else one with
+// more steps in flight.
+template <int WORDS, int NT>
+constexpr int kWavesPerSimd = WORDS == 2 && NT == 1 ? 4 : 2;
+template <int WORDS, int NT>
+constexpr int kStepsAhead = WORDS == 1 && NT == 1 ? 3 : 2;
+
+// ------------------------------------------------------------------ gate and up
+
+// One workgroup: one expert and 32 consecutive h values (the quantization block of the
+// down projection's input).  Wave w takes rows 16 (w / 4) .. of gate and of up, and
+// steps w % 4, w % 4 + 4, ..; the four parts of a sum are added in order.  NT token
+// tiles a pass.
+template <int WORDS, int NT>
+__global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_gate_up_mma_kernel(MoeArgs a) {
+    using T = Tile<WORDS>;
+    constexpr int kTokens = NT * T::kTokens;
+    constexpr int kAhead = kStepsAhead<WORDS, NT>;
+    __shared__ double part[kWaves][2][NT][T::kVals][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int act = static_cast<int>(blockIdx.x) / a.nbf, hb = static_cast<int>(blockIdx.x) % a.nbf;
+    if (act >= a.plan->n_active) return;
+    const MoeEntry en = a.plan->entry[act];
+    const int count = __popcll(en.mask);
+    const int64_t row0 = static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave >> 2) * kTileRows;
+    const __amdgpu_buffer_rsrc_t gate = weight_tile(a.w_gate, row0, a.nbk), up = weight_tile(a.w_up, row0, a.nbk);
+    const __amdgpu_buffer_rsrc_t words = buffer_of(a.xq, a.rows * a.sbk * (WORDS * 32));
+    const __amdgpu_buffer_rsrc_t scales = buffer_of(a.xs, a.rows * a.sbk * 4);
+    const uint32_t lane_off = (lane & 15) * static_cast<uint32_t>(a.nbk) * kBlockBytes + (((lane >> 4) * kBlockBytes) & ~3u);
+    const int w_end = (a.nbk - (lane >> 4) + kStepBlocks - 1) / kStepBlocks;  // steps in which the lane has a block
+    const int steps = a.sbk / kStepBlocks;
+    for (int c0 = 0; c0 < count; c0 += kTokens) {
+        ActOffsets<WORDS> ao[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            ao[t] = act_offsets<WORDS>(a.sbk, lane, [&](int i) {
+                const int at = c0 + t * T::kTokens + i;
+                return at < count ? a.plan->pair_token[en.offset + at] : -1;
+            });
+        double acc[2][NT][T::kVals];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int v = 0; v < T::kVals; ++v) acc[m][t][v] = 0.0;
+        struct {
+            Window gate, up;
+            Acts<WORDS> acts[NT];
+        } ring[kAhead];
+        auto load = [&](int p, int step) {
+            load_weights(gate, lane_off, step, step < w_end, ring[p].gate);
+            load_weights(up, lane_off, step, step < w_end, ring[p].up);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) load_acts<WORDS>(words, scales, ao[t], step, step < steps, ring[p].acts[t]);
+        };
+        const int first = wave & 3;
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) load(p, first + 4 * p);
+#pragma clang loop unroll(disable)
+        for (int s0 = first; s0 < steps; s0 += 4 * kAhead) {
+#pragma unroll
+            for (int p = 0; p < kAhead; ++p) {
+                Operands o;
+                operands_of(ring[p].gate, lane, o);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[0][t]);
+                operands_of(ring[p].up, lane, o);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[1][t]);
+                load(p, s0 + 4 * (p + kAhead));
+                __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time in registers
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int v = 0; v < T::kVals; ++v) part[wave][m][t][v][lane] = acc[m][t][v];
+        __syncthreads();
+        // a thread forms one h value; the 32 of a token quantize their block as quantize4 does
+        const int n = min(kTokens, count - c0);
+        for (int i = threadIdx.x; i < n * kHBlock; i += kThreads) {
+            const int token = i / kHBlock, row = i % kHBlock;
+            const int t = token / T::kTokens, in = token % T::kTokens;
+            const int from = (in / T::kVals) * 16 + (row & 15), v = in % T::kVals;
+            double sums[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int w0 = (row >> 4) * 4;
+                sums[m] = ((part[w0][m][t][v][from] + part[w0 + 1][m][t][v][from]) + part[w0 + 2][m][t][v][from]) +
+                          part[w0 + 3][m][t][v][from];
+            }
+            const double post = WORDS == 2 ? 1.0 / 128.0 : 1.0;
+            const double g = static_cast<double>(static_cast<float>(sums[0] * post));
+            const double u = static_cast<double>(static_cast<float>(sums[1] * post));
+            const float h = static_cast<float>(g / (1.0 + exp(-g)) * u);
+            float amax = fabsf(h);
+#pragma unroll
+            for (int off = 1; off < kHBlock; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+            const float s = amax / 127.0f;
+            const int q = s == 0.0f ? 0 : quant_clamped(h / s);
+            const int64_t pair = en.offset + c0 + token;
+            uint8_t *rec = a.hq + pair * a.sbf * (WORDS * 32);
+            rec[record_offset(1, WORDS, hb, 0, row >> 2) + (row & 3)] = static_cast<uint8_t>(q);
+            if constexpr (WORDS == 2) {
+                const float rest = __builtin_fmaf(-s, static_cast<float>(q), h);
+                const int l = s == 0.0f ? 0 : quant_clamped((rest * 128.0f) / s);
+                rec[record_offset(1, WORDS, hb, 1, row >> 2) + (row & 3)] = static_cast<uint8_t>(l);
+            }
+            if (row == 0) a.hs[pair * a.sbf + hb] = s;
+            // the blocks that round the row up to four have scale 0 (their words meet zero weights)
+            if (hb == a.nbf - 1 && row < a.sbf - a.nbf) a.hs[pair * a.sbf + a.nbf + row] = 0.f;
+        }
+        if (c0 + kTokens < count) __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------------- down
+
+// A tile of 16 output columns of y for every token, by a.splits workgroups.  The chosen
+// experts' steps, laid end to end, are split evenly over the workgroups' waves; a wave
+// adds gate * (its part of a product) to its own f64 sums [rows][16], the waves' sums
+// are added in wave order, and the workgroups' sums (through the workspace, by the last
+// to arrive) in their order: the order of every sum depends on the choices alone.
+template <int WORDS, int NT>
+__global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_down_mma_kernel(MoeArgs a) {
+    using T = Tile<WORDS>;
+    constexpr int kTokens = NT * T::kTokens;
+    constexpr int kAhead = kStepsAhead<WORDS, NT>;
+    extern __shared__ __align__(16) double sums[];  // [waves][rows][16]
+    __shared__ int is_last;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = static_cast<int>(blockIdx.x) / a.splits, split = static_cast<int>(blockIdx.x) % a.splits;
+    const int row0 = tile * kTileRows;
+    const int outs = a.rows * kTileRows;
+    double *mine = sums + wave * outs;
+    for (int i = lane; i < outs; i += 64) mine[i] = 0.0;
+    wave_lds_sync();
+    const int steps = a.sbf / kStepBlocks;
+    const int total = a.plan->n_active * steps;
+    const int me = split * kWaves + wave, all = a.splits * kWaves;
+    const int from = static_cast<int>(static_cast<int64_t>(total) * me / all);
+    const int to = static_cast<int>(static_cast<int64_t>(total) * (me + 1) / all);
+    const __amdgpu_buffer_rsrc_t words = buffer_of(a.hq, a.rows * a.top_k * a.sbf * (WORDS * 32));
+    const __amdgpu_buffer_rsrc_t scales = buffer_of(a.hs, a.rows * a.top_k * a.sbf * 4);
+    const uint32_t lane_off = (lane & 15) * static_cast<uint32_t>(a.nbf) * kBlockBytes + (((lane >> 4) * kBlockBytes) & ~3u);
+    const int w_end = (a.nbf - (lane >> 4) + kStepBlocks - 1) / kStepBlocks;
+    const double post = WORDS == 2 ? 1.0 / 128.0 : 1.0;
+    for (int at = from; at < to;) {
+        const int act = at / steps, st0 = at - act * steps;
+        const int st1 = min(steps, st0 + to - at);
+        at += st1 - st0;
+        const MoeEntry en = a.plan->entry[act];
+        const int count = __popcll(en.mask);
+        const __amdgpu_buffer_rsrc_t wt = weight_tile(a.w_down, static_cast<int64_t>(en.expert) * a.k + row0, a.nbf);
+        for (int c0 = 0; c0 < count; c0 += kTokens) {
+            ActOffsets<WORDS> ao[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                ao[t] = act_offsets<WORDS>(a.sbf, lane, [&](int i) {
+                    const int p = c0 + t * T::kTokens + i;
+                    return p < count ? en.offset + p : -1;
+                });
+            double acc[NT][T::kVals];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int v = 0; v < T::kVals; ++v) acc[t][v] = 0.0;
+            struct {
+                Window w;
+                Acts<WORDS> acts[NT];
+            } ring[kAhead];
+            auto load = [&](int p, int step) {
+                load_weights(wt, lane_off, step, step < min(st1, w_end), ring[p].w);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) load_acts<WORDS>(words, scales, ao[t], step, step < st1, ring[p].acts[t]);
+            };
+#pragma unroll
+            for (int p = 0; p < kAhead; ++p) load(p, st0 + p);
+#pragma clang loop unroll(disable)
+            for (int s0 = st0; s0 < st1; s0 += kAhead) {
+#pragma unroll
+                for (int p = 0; p < kAhead; ++p) {
+                    Operands o;
+                    operands_of(ring[p].w, lane, o);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[t]);
+                    load(p, s0 + p + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int v = 0; v < T::kVals; ++v) {
+                    const int p = c0 + t * T::kTokens + (lane >> 4) * T::kVals + v;
+                    if (p < count)
+                        mine[a.plan->pair_token[en.offset + p] * kTileRows + (lane & 15)] +=
+                            a.plan->pair_gate[en.offset + p] * (acc[t][v] * post);
+                }
+        }
+    }
+    __syncthreads();
+    double *parts = a.parts + static_cast<int64_t>(tile) * a.splits * outs;
+    if (a.splits > 1) {
+        // agent-scope stores, complete before this workgroup counts itself in
+        for (int i = threadIdx.x; i < outs; i += kThreads) {
+            double v = 0.0;
+            for (int w = 0; w < kWaves; ++w) v += sums[w * outs + i];
+            __hip_atomic_store(parts + static_cast<int64_t>(split) * outs + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint32_t *counter = a.counters + kMoeTileCounter + tile;
+            const uint32_t done = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            is_last = done == static_cast<uint32_t>(a.splits) - 1;
+            if (is_last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!is_last) return;
+    }
+    for (int i = threadIdx.x; i < outs; i += kThreads) {
+        double v = 0.0;
+        if (a.splits > 1) {
+            for (int s = 0; s < a.splits; ++s)
+                v += __hip_atomic_load(parts + static_cast<int64_t>(s) * outs + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+            for (int w = 0; w < kWaves; ++w) v += sums[w * outs + i];
+        }
+        const int64_t o = static_cast<int64_t>(i / kTileRows) * a.k + row0 + i % kTileRows;
+        if (a.residual) v += static_cast<double>(a.residual[o]);
+        a.y[o] = static_cast<float>(v);
+    }
+}
+
+template <int WORDS, int NT>
+hipError_t run(const MoeArgs &a, hipStream_t stream) {
+    const int most = std::min(a.experts, a.rows * a.top_k);
+    moe_gate_up_mma_kernel<WORDS, NT><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const size_t lds = static_cast<size_t>(kWaves) * a.rows * kTileRows * sizeof(double);
+    moe_down_mma_kernel<WORDS, NT><<<dim3(a.k / kTileRows * a.splits), kThreads, lds, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int WORDS>
+hipError_t run_words(const MoeArgs &a, hipStream_t stream) {
+    // token tiles a pass, by the mean number of tokens an expert gets
+    const int mean = a.rows * a.top_k / a.experts;
+    return 2 * mean > Tile<WORDS>::kTokens ? run<WORDS, 2>(a, stream) : run<WORDS, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_moe_mma(int mode, const MoeArgs &a, hipStream_t stream) {
+    return mode == 2 ? run_words<2>(a, stream) : run_words<1>(a, stream);
+}
+
+}  // namespace q8

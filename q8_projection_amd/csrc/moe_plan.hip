@@ -246,15 +246,17 @@ __global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int qu
         if (static_cast<int>(blockIdx.x) < quant_wgs) {
             const int t = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
             const int blk = t / kQuantLanes, part = t % kQuantLanes;
-            const bool valid = blk < a.rows * a.nbk;
+            const int row = blk / a.sbk, b = blk - row * a.sbk;
+            const bool valid = row < a.rows;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid) v = reinterpret_cast<const float4 *>(a.x)[t];
+            if (valid && b < a.nbk)
+                v = *reinterpret_cast<const float4 *>(a.x + static_cast<int64_t>(row) * a.k + b * kBlock + 4 * part);
             uint32_t h4, l4;
             const float s = quantize4<WORDS>(v, h4, l4);
             if (!valid) return;
-            uint32_t *rec = reinterpret_cast<uint32_t *>(a.xq + static_cast<int64_t>(blk) * (WORDS * 32));
-            rec[part] = h4;
-            if (WORDS == 2) rec[8 + part] = l4;
+            uint8_t *rec = a.xq + static_cast<int64_t>(row) * a.sbk * (WORDS * 32);
+            *reinterpret_cast<uint32_t *>(rec + record_offset(a.tiled, WORDS, b, 0, part)) = h4;
+            if (WORDS == 2) *reinterpret_cast<uint32_t *>(rec + record_offset(a.tiled, WORDS, b, 1, part)) = l4;
             if (part == 0) a.xs[blk] = s;
             return;
         }
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void moe_prepare_kernel(MoeArgs a, int qu
 
 hipError_t launch_moe(int mode, const MoeArgs &a, bool route, bool experts, hipStream_t stream) {
     const int quant_wgs =
-        experts && mode != 0 ? (a.rows * a.nbk * kQuantLanes + kThreads - 1) / kThreads : 0;
+        experts && mode != 0 ? (a.rows * a.sbk * kQuantLanes + kThreads - 1) / kThreads : 0;
     const int groups = (a.rows + kTokenGroup - 1) / kTokenGroup;
     const dim3 grid(quant_wgs + (route ? a.experts * groups : 1));
     if (mode == 2)
