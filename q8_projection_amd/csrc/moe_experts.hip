@@ -150,9 +150,9 @@ struct GateUpShared {
 // One pass: the wave's 8 rows of gate or up times n <= TG tokens, into s.gu.
 template <int WORDS, int TG, typename S>
 __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t first_row, const ActSource &src,
-                                             const int *rows, int n, int lane, int wave) {
+                                             const int *tokens, int n, int lane, int wave) {
     constexpr int C = kChunk<WORDS>, R = kRec<WORDS>;
-    constexpr int kAhead = WORDS == 0 ? 3 : TG == 4 ? 4 : 6;  // windows in flight
+    constexpr int kAhead = 4;  // windows in flight (3, 6 and 8 measured slower)
     static_assert(C * R <= kThreads * 16 && C * TG <= kThreads, "a load a thread and token, a scale a thread");
     const int tid = threadIdx.x;
     double acc[TG];
@@ -160,9 +160,16 @@ __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t fir
     for (int t = 0; t < TG; ++t) acc[t] = 0.0;
     for (int b0 = 0; b0 < src.nb; b0 += C) {
         const int nblk = min(C, src.nb - b0), steps = (nblk + kStepBlocks - 1) / kStepBlocks;
-        // the chunk's activations (zeros behind the row's last block), then the first
-        // windows: the loads come back in this order, so the wait for the activations
-        // leaves the windows in flight
+        // the first windows, which need nothing but the expert, then the tokens and the
+        // chunk's activations (zeros behind the row's last block)
+        Weights wt(w, first_row, src.nb, b0 / kStepBlocks, b0 / kStepBlocks + steps, lane);
+        Window ring[kAhead];
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) wt.next(ring[p]);
+        __builtin_amdgcn_sched_barrier(0);
+        int rows[TG];
+#pragma unroll
+        for (int t = 0; t < TG; ++t) rows[t] = tokens ? tokens[min(t, n - 1)] : 0;
         uint4 v[TG];
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
@@ -177,10 +184,6 @@ __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t fir
             for (int u = 1; u < TG; ++u) row = t == u ? rows[u] : row;
             sc = load_float(src.scales, t < n && i < nblk ? (static_cast<uint32_t>(row) * src.nb + b0 + i) * 4 : kOob);
         }
-        Weights wt(w, first_row, src.nb, b0 / kStepBlocks, b0 / kStepBlocks + steps, lane);
-        Window ring[kAhead];
-#pragma unroll
-        for (int p = 0; p < kAhead; ++p) wt.next(ring[p]);
         if (b0 > 0) lds_barrier();  // the last chunk has been read
 #pragma unroll
         for (int t = 0; t < TG; ++t)
@@ -221,24 +224,24 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_ke
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nhb = a.nbf;
     const int act = static_cast<int>(blockIdx.x) / nhb, hb = static_cast<int>(blockIdx.x) % nhb;
-    if (act >= a.plan->n_active) return;
+    // both loads at once (an entry behind the last is left over from another call)
     const MoeEntry en = a.plan->entry[act];
+    const int n_active = a.plan->n_active;
+    asm volatile("" ::"s"(en.expert), "s"(n_active));
+    if (act >= n_active) return;
     const int count = ONE ? 1 : __popcll(en.mask);
     const uint8_t *w = wave < 4 ? a.w_gate : a.w_up;
     const int64_t first_row = static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave & 3) * kTileRows;
     const ActSource src = act_source<WORDS>(WORDS ? static_cast<const void *>(a.xq) : a.x, a.xs, a.rows, a.nbk);
     for (int c0 = 0; c0 < count; c0 += MAX_TG) {
         const int n = min(MAX_TG, count - c0);
-        int rows[MAX_TG];
-#pragma unroll
-        for (int t = 0; t < MAX_TG; ++t)
-            rows[t] = ONE ? 0 : __builtin_amdgcn_readfirstlane(a.plan->pair_token[en.offset + c0 + min(t, n - 1)]);
+        const int *tokens = ONE ? nullptr : a.plan->pair_token + en.offset + c0;
         if (MAX_TG == 1 || n == 1)
-            gate_up_pass<WORDS, 1>(s, w, first_row, src, rows, n, lane, wave);
+            gate_up_pass<WORDS, 1>(s, w, first_row, src, tokens, n, lane, wave);
         else if (MAX_TG > 1 && n == 2)
-            gate_up_pass<WORDS, MAX_TG == 1 ? 1 : 2>(s, w, first_row, src, rows, n, lane, wave);
+            gate_up_pass<WORDS, MAX_TG == 1 ? 1 : 2>(s, w, first_row, src, tokens, n, lane, wave);
         else
-            gate_up_pass<WORDS, MAX_TG>(s, w, first_row, src, rows, n, lane, wave);
+            gate_up_pass<WORDS, MAX_TG>(s, w, first_row, src, tokens, n, lane, wave);
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < n * kHBlock) {
             const int t = threadIdx.x / kHBlock, i = threadIdx.x % kHBlock;
