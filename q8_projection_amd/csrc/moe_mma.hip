@@ -175,100 +175,163 @@ __device__ __forceinline__ void multiply(const Operands &w, const Acts<WORDS> &a
     }
 }
 
-// Two workgroups a CU where the registers of one token tile allow it, else one with
-// more steps in flight.
-template <int WORDS, int NT>
-constexpr int kWavesPerSimd = WORDS == 2 && NT == 1 ? 4 : 2;
-template <int WORDS, int NT>
-constexpr int kStepsAhead = WORDS == 1 && NT == 1 ? 3 : 2;
-
 // ------------------------------------------------------------------ gate and up
 
-// One workgroup: one expert and 32 consecutive h values (the quantization block of the
-// down projection's input).  Wave w takes rows 16 (w / 4) .. of gate and of up, and
-// steps w % 4, w % 4 + 4, ..; the four parts of a sum are added in order.  NT token
-// tiles a pass.
+// Blocks of the tokens' rows that are in LDS at a time, for all waves, and the bytes
+// between two rows there: 16 past a multiple of 128, so that the 16 columns' parts lie
+// on different banks.
+constexpr int kChunk = 64;  // blocks
+template <int WORDS>
+constexpr int kRowBytes = kChunk * WORDS * 32 + 16;
+
+constexpr int kParts = 2;                // waves that share the steps of a tile
+constexpr int kGuWaves = 2 * kParts;     // small workgroups: two a CU, one's start and end beside the other's steps
+constexpr int kGuThreads = 64 * kGuWaves;
+
 template <int WORDS, int NT>
-__global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_gate_up_mma_kernel(MoeArgs a) {
+struct GateUpShared {
+    static constexpr int kTokens = NT * Tile<WORDS>::kTokens;
+    union {
+        struct {
+            uint8_t words[kTokens][kRowBytes<WORDS>];
+            float scales[kTokens][kChunk];
+        };
+        double part[kGuWaves][2][NT][Tile<WORDS>::kVals][64];
+    };
+};
+
+// One workgroup: one expert and 32 consecutive h values (the quantization block of the
+// down projection's input).  Wave w takes rows 16 (w / 2) .. of gate and of up, and
+// every second step from w % 2 on; the two parts of a sum are added in order.  A pass takes
+// up to NT token tiles; their rows are staged in LDS once for all waves, behind the
+// first weight loads, so that the registers hold weights only.
+template <int WORDS, int NT>
+__global__ __launch_bounds__(kGuThreads, 2) void moe_gate_up_mma_kernel(MoeArgs a) {
     using T = Tile<WORDS>;
-    constexpr int kTokens = NT * T::kTokens;
-    constexpr int kAhead = kStepsAhead<WORDS, NT>;
-    __shared__ double part[kWaves][2][NT][T::kVals][64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    using S = GateUpShared<WORDS, NT>;
+    constexpr int kTokens = S::kTokens, C = kChunk, kAhead = 1;
+    __shared__ __align__(16) S s;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int act = static_cast<int>(blockIdx.x) / a.nbf, hb = static_cast<int>(blockIdx.x) % a.nbf;
-    if (act >= a.plan->n_active) return;
+    // both loads at once (an entry behind the last is left over from another call)
     const MoeEntry en = a.plan->entry[act];
+    const int n_active = a.plan->n_active;
+    asm volatile("" ::"s"(en.expert), "s"(n_active));
+    if (act >= n_active) return;
     const int count = __popcll(en.mask);
-    const int64_t row0 = static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave >> 2) * kTileRows;
+    const int64_t row0 = static_cast<int64_t>(en.expert) * a.ff + hb * kHBlock + (wave / kParts) * kTileRows;
     const __amdgpu_buffer_rsrc_t gate = weight_tile(a.w_gate, row0, a.nbk), up = weight_tile(a.w_up, row0, a.nbk);
     const __amdgpu_buffer_rsrc_t words = buffer_of(a.xq, a.rows * a.sbk * (WORDS * 32));
     const __amdgpu_buffer_rsrc_t scales = buffer_of(a.xs, a.rows * a.sbk * 4);
     const uint32_t lane_off = (lane & 15) * static_cast<uint32_t>(a.nbk) * kBlockBytes + (((lane >> 4) * kBlockBytes) & ~3u);
     const int w_end = (a.nbk - (lane >> 4) + kStepBlocks - 1) / kStepBlocks;  // steps in which the lane has a block
-    const int steps = a.sbk / kStepBlocks;
+    const int m = lane & 15, q = lane >> 4;
+    const int32_t *tokens = a.plan->pair_token + en.offset;
     for (int c0 = 0; c0 < count; c0 += kTokens) {
-        ActOffsets<WORDS> ao[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            ao[t] = act_offsets<WORDS>(a.sbk, lane, [&](int i) {
-                const int at = c0 + t * T::kTokens + i;
-                return at < count ? a.plan->pair_token[en.offset + at] : -1;
-            });
+        const int n = min(kTokens, count - c0);
         double acc[2][NT][T::kVals];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int v = 0; v < T::kVals; ++v) acc[m][t][v] = 0.0;
-        struct {
-            Window gate, up;
-            Acts<WORDS> acts[NT];
-        } ring[kAhead];
-        auto load = [&](int p, int step) {
-            load_weights(gate, lane_off, step, step < w_end, ring[p].gate);
-            load_weights(up, lane_off, step, step < w_end, ring[p].up);
+                for (int v = 0; v < T::kVals; ++v) acc[w][t][v] = 0.0;
+        for (int b0 = 0; b0 < a.sbk; b0 += C) {
+            const int nblk = min(C, a.sbk - b0), step0 = b0 / kStepBlocks, steps = nblk / kStepBlocks;
+            Window ring[kAhead][2];
+            auto load = [&](int p, int w, int step) {
+                load_weights(w ? up : gate, lane_off, step0 + step, step < steps && step0 + step < w_end, ring[p][w]);
+            };
+            const int first = wave % kParts;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) load_acts<WORDS>(words, scales, ao[t], step, step < steps, ring[p].acts[t]);
-        };
-        const int first = wave & 3;
+            for (int p = 0; p < kAhead; ++p)
 #pragma unroll
-        for (int p = 0; p < kAhead; ++p) load(p, first + 4 * p);
+                for (int w = 0; w < 2; ++w) load(p, w, first + kParts * p);
+            __builtin_amdgcn_sched_barrier(0);
+            // 16 bytes a thread and load, every load in flight at once: the rows' words,
+            // then their scales
+            constexpr int kUnits = C * WORDS * 2, kStep = kGuThreads / kUnits, kLoads = kTokens / kStep;
+            constexpr int kScaleUnits = C / 4, kScaleStep = kGuThreads / kScaleUnits, kScaleLoads = (kTokens + kScaleStep - 1) / kScaleStep;
+            static_assert(kGuThreads % kUnits == 0 && kTokens % kStep == 0, "whole rows");
+            const int unit = tid % kUnits, scale_unit = tid % kScaleUnits;
+            uint32_t row[kLoads], scale_row[kScaleLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) row[k] = static_cast<uint32_t>(tokens[c0 + min(tid / kUnits + k * kStep, n - 1)]);
+#pragma unroll
+            for (int k = 0; k < kScaleLoads; ++k)
+                scale_row[k] = static_cast<uint32_t>(tokens[c0 + min(tid / kScaleUnits + k * kScaleStep, n - 1)]);
+            u32x4 d[kLoads], ds[kScaleLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const bool ok = k * kStep < n && unit * 16 < nblk * WORDS * 32;
+                d[k] = __builtin_amdgcn_raw_buffer_load_b128(words, ok ? (row[k] * a.sbk + b0) * (WORDS * 32) + unit * 16 : kOob, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kScaleLoads; ++k)
+                ds[k] = __builtin_amdgcn_raw_buffer_load_b128(
+                    scales, scale_unit * 4 < nblk ? (scale_row[k] * a.sbk + b0 + scale_unit * 4) * 4 : kOob, 0, 0);
+            if (c0 > 0 || b0 > 0) __syncthreads();  // what was there has been read
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                *reinterpret_cast<u32x4 *>(s.words[tid / kUnits + k * kStep] + unit * 16) = d[k];
+#pragma unroll
+            for (int k = 0; k < kScaleLoads; ++k)
+                if (tid / kScaleUnits + k * kScaleStep < kTokens)
+                    *reinterpret_cast<u32x4 *>(&s.scales[tid / kScaleUnits + k * kScaleStep][scale_unit * 4]) = ds[k];
+            __syncthreads();
 #pragma clang loop unroll(disable)
-        for (int s0 = first; s0 < steps; s0 += 4 * kAhead) {
+            for (int s0 = first; s0 < steps; s0 += kParts * kAhead) {
 #pragma unroll
-            for (int p = 0; p < kAhead; ++p) {
-                Operands o;
-                operands_of(ring[p].gate, lane, o);
+                for (int p = 0; p < kAhead; ++p) {
+                    const int st = min(s0 + kParts * p, steps - 1);  // (a step behind the last has zero weights)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[0][t]);
-                operands_of(ring[p].up, lane, o);
+                    for (int w = 0; w < 2; ++w) {
+                        Operands o;
+                        operands_of(ring[p][w], lane, o);
+                        load(p, w, s0 + kParts * (p + kAhead));
 #pragma unroll
-                for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[1][t]);
-                load(p, s0 + 4 * (p + kAhead));
-                __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time in registers
+                        for (int t = 0; t < NT; ++t) {
+                            if (t * T::kTokens >= n) break;  // the same for the workgroup
+                            Acts<WORDS> x;
+                            // columns without a token repeat the last one: their sums are not used
+                            const uint8_t *row = s.words[min(t * T::kTokens + T::token(m), n - 1)] + st * (WORDS * 128) + T::word(m) * 128 + q * 32;
+                            const ulonglong2 p0 = reinterpret_cast<const ulonglong2 *>(row)[0], p1 = reinterpret_cast<const ulonglong2 *>(row)[1];
+                            x.part[0] = static_cast<long>(p0.x); x.part[1] = static_cast<long>(p0.y);
+                            x.part[2] = static_cast<long>(p1.x); x.part[3] = static_cast<long>(p1.y);
+#pragma unroll
+                            for (int v = 0; v < T::kVals; ++v) {
+                                const float4 sv = *reinterpret_cast<const float4 *>(
+                                    &s.scales[min(t * T::kTokens + q * T::kVals + v, n - 1)][st * 4]);
+                                x.s[v][0] = sv.x; x.s[v][1] = sv.y; x.s[v][2] = sv.z; x.s[v][3] = sv.w;
+                            }
+                            multiply<WORDS>(o, x, acc[w][t]);
+                            __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time in registers
+                        }
+                    }
+                }
             }
         }
+        __syncthreads();  // the activations have been read
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int v = 0; v < T::kVals; ++v) part[wave][m][t][v][lane] = acc[m][t][v];
+                for (int v = 0; v < T::kVals; ++v) s.part[wave][w][t][v][lane] = acc[w][t][v];
         __syncthreads();
         // a thread forms one h value; the 32 of a token quantize their block as quantize4 does
-        const int n = min(kTokens, count - c0);
-        for (int i = threadIdx.x; i < n * kHBlock; i += kThreads) {
+        for (int i = threadIdx.x; i < n * kHBlock; i += kGuThreads) {
             const int token = i / kHBlock, row = i % kHBlock;
             const int t = token / T::kTokens, in = token % T::kTokens;
             const int from = (in / T::kVals) * 16 + (row & 15), v = in % T::kVals;
             double sums[2];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const int w0 = (row >> 4) * 4;
-                sums[m] = ((part[w0][m][t][v][from] + part[w0 + 1][m][t][v][from]) + part[w0 + 2][m][t][v][from]) +
-                          part[w0 + 3][m][t][v][from];
+                const int w0 = (row >> 4) * kParts;
+                sums[m] = s.part[w0][m][t][v][from];
+#pragma unroll
+                for (int w = 1; w < kParts; ++w) sums[m] += s.part[w0 + w][m][t][v][from];
             }
             const double post = WORDS == 2 ? 1.0 / 128.0 : 1.0;
             const double g = static_cast<double>(static_cast<float>(sums[0] * post));
@@ -277,21 +340,20 @@ __global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_gate
             float amax = fabsf(h);
 #pragma unroll
             for (int off = 1; off < kHBlock; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-            const float s = amax / 127.0f;
-            const int q = s == 0.0f ? 0 : quant_clamped(h / s);
+            const float sc = amax / 127.0f;
+            const int hi = sc == 0.0f ? 0 : quant_clamped(h / sc);
             const int64_t pair = en.offset + c0 + token;
             uint8_t *rec = a.hq + pair * a.sbf * (WORDS * 32);
-            rec[record_offset(1, WORDS, hb, 0, row >> 2) + (row & 3)] = static_cast<uint8_t>(q);
+            rec[record_offset(1, WORDS, hb, 0, row >> 2) + (row & 3)] = static_cast<uint8_t>(hi);
             if constexpr (WORDS == 2) {
-                const float rest = __builtin_fmaf(-s, static_cast<float>(q), h);
-                const int l = s == 0.0f ? 0 : quant_clamped((rest * 128.0f) / s);
+                const float rest = __builtin_fmaf(-sc, static_cast<float>(hi), h);
+                const int l = sc == 0.0f ? 0 : quant_clamped((rest * 128.0f) / sc);
                 rec[record_offset(1, WORDS, hb, 1, row >> 2) + (row & 3)] = static_cast<uint8_t>(l);
             }
-            if (row == 0) a.hs[pair * a.sbf + hb] = s;
+            if (row == 0) a.hs[pair * a.sbf + hb] = sc;
             // the blocks that round the row up to four have scale 0 (their words meet zero weights)
             if (hb == a.nbf - 1 && row < a.sbf - a.nbf) a.hs[pair * a.sbf + a.nbf + row] = 0.f;
         }
-        if (c0 + kTokens < count) __syncthreads();
     }
 }
 
@@ -303,10 +365,10 @@ __global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_gate
 // are added in wave order, and the workgroups' sums (through the workspace, by the last
 // to arrive) in their order: the order of every sum depends on the choices alone.
 template <int WORDS, int NT>
-__global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_down_mma_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_down_mma_kernel(MoeArgs a) {
     using T = Tile<WORDS>;
     constexpr int kTokens = NT * T::kTokens;
-    constexpr int kAhead = kStepsAhead<WORDS, NT>;
+    constexpr int kAhead = 2;
     extern __shared__ __align__(16) double sums[];  // [waves][rows][16]
     __shared__ int is_last;
     const int lane = threadIdx.x & 63;
@@ -354,7 +416,8 @@ __global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_down
             auto load = [&](int p, int step) {
                 load_weights(wt, lane_off, step, step < min(st1, w_end), ring[p].w);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) load_acts<WORDS>(words, scales, ao[t], step, step < st1, ring[p].acts[t]);
+                for (int t = 0; t < NT; ++t)
+                    if (c0 + t * T::kTokens < count) load_acts<WORDS>(words, scales, ao[t], step, step < st1, ring[p].acts[t]);
             };
 #pragma unroll
             for (int p = 0; p < kAhead; ++p) load(p, st0 + p);
@@ -365,7 +428,8 @@ __global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_down
                     Operands o;
                     operands_of(ring[p].w, lane, o);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) multiply<WORDS>(o, ring[p].acts[t], acc[t]);
+                    for (int t = 0; t < NT; ++t)
+                        if (c0 + t * T::kTokens < count) multiply<WORDS>(o, ring[p].acts[t], acc[t]);
                     load(p, s0 + p + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -418,7 +482,7 @@ __global__ __launch_bounds__(kThreads, (kWavesPerSimd<WORDS, NT>)) void moe_down
 template <int WORDS, int NT>
 hipError_t run(const MoeArgs &a, hipStream_t stream) {
     const int most = std::min(a.experts, a.rows * a.top_k);
-    moe_gate_up_mma_kernel<WORDS, NT><<<dim3(static_cast<unsigned>(most) * a.nbf), kThreads, 0, stream>>>(a);
+    moe_gate_up_mma_kernel<WORDS, NT><<<dim3(static_cast<unsigned>(most) * a.nbf), kGuThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const size_t lds = static_cast<size_t>(kWaves) * a.rows * kTileRows * sizeof(double);
     moe_down_mma_kernel<WORDS, NT><<<dim3(a.k / kTileRows * a.splits), kThreads, lds, stream>>>(a);
