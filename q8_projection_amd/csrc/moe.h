@@ -58,7 +58,7 @@ struct MoeArgs {
     int sbk, sbf;           // blocks of one row of xq and hq: nbk and nbf, rounded up to four if tiled
     int splits;             // workgroups that share a tile of the down projection
     // workspace
-    double *parts;          // [splits][k / 16][rows][16] partial outputs (splits > 1)
+    double *parts;          // [k / 32][splits][rows][32] partial outputs (splits > 1)
     uint32_t *counters;     // zero between calls
     MoePlan *plan;
     float *logits;          // [rows][experts]
@@ -81,12 +81,15 @@ __host__ __device__ inline int record_offset(int tiled, int words, int blk, int 
 // four tokens an expert.
 inline int moe_tiled(int words, const MoeArgs &a) { return words > 0 && a.rows * a.top_k > 4 * a.experts; }
 
-// Workgroups that share a tile of 16 output columns in the down projection on the
+// Output columns of a workgroup of the down projection on the matrix cores.
+constexpr int kMoeDownRows = 32;
+
+// Workgroups that share a tile of them in the down projection on the
 // matrix cores: enough for two workgroups a CU.
 inline int moe_down_splits(const MoeArgs &a) {
     if (!a.tiled) return 1;
     int s = 1;
-    while (s < kMoeMaxSplits && a.k / 16 * s < 512) s *= 2;
+    while (s < kMoeMaxSplits && a.k / kMoeDownRows * s < 512) s *= 2;
     return s;
 }
 

@@ -24,8 +24,6 @@
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kTileRows = 16;
 constexpr int kStepBlocks = 4;
 constexpr int kHBlock = 32;  // h values of one workgroup of the gate/up kernel: one quantization block
@@ -359,29 +357,35 @@ __global__ __launch_bounds__(kGuThreads, 2) void moe_gate_up_mma_kernel(MoeArgs 
 
 // ------------------------------------------------------------------------- down
 
-// A tile of 16 output columns of y for every token, by a.splits workgroups.  The chosen
+// A tile of 32 output columns of y for every token, by a.splits workgroups.  The chosen
 // experts' steps, laid end to end, are split evenly over the workgroups' waves; a wave
-// adds gate * (its part of a product) to its own f64 sums [rows][16], the waves' sums
+// adds gate * (its part of a product) to its own f64 sums [rows][32], the waves' sums
 // are added in wave order, and the workgroups' sums (through the workspace, by the last
 // to arrive) in their order: the order of every sum depends on the choices alone.
+constexpr int kDownWaves = 4, kDownThreads = 64 * kDownWaves;
+static_assert(kMoeDownRows == 2 * kTileRows, "two tiles a wave");
+
 template <int WORDS, int NT>
-__global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_down_mma_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kDownThreads, 2) void moe_down_mma_kernel(MoeArgs a) {
     using T = Tile<WORDS>;
     constexpr int kTokens = NT * T::kTokens;
-    constexpr int kAhead = 2;
-    extern __shared__ __align__(16) double sums[];  // [waves][rows][16]
+    constexpr int kAhead = 1;
+    extern __shared__ __align__(16) double sums[];  // [waves][rows][32]
     __shared__ int is_last;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tile = static_cast<int>(blockIdx.x) / a.splits, split = static_cast<int>(blockIdx.x) % a.splits;
-    const int row0 = tile * kTileRows;
-    const int outs = a.rows * kTileRows;
+    // workgroups in turn take different tiles of the same part: every XCD then has a share of
+    // each expert (72 us where an XCD had experts of its own, 69 so)
+    const int tiles = a.k / kMoeDownRows;
+    const int tile = static_cast<int>(blockIdx.x) % tiles, split = static_cast<int>(blockIdx.x) / tiles;
+    const int row0 = tile * kMoeDownRows;
+    const int outs = a.rows * kMoeDownRows;
     double *mine = sums + wave * outs;
     for (int i = lane; i < outs; i += 64) mine[i] = 0.0;
     wave_lds_sync();
     const int steps = a.sbf / kStepBlocks;
     const int total = a.plan->n_active * steps;
-    const int me = split * kWaves + wave, all = a.splits * kWaves;
+    const int me = split * kDownWaves + wave, all = a.splits * kDownWaves;
     const int from = static_cast<int>(static_cast<int64_t>(total) * me / all);
     const int to = static_cast<int>(static_cast<int64_t>(total) * (me + 1) / all);
     const __amdgpu_buffer_rsrc_t words = buffer_of(a.hq, a.rows * a.top_k * a.sbf * (WORDS * 32));
@@ -395,7 +399,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
         at += st1 - st0;
         const MoeEntry en = a.plan->entry[act];
         const int count = __popcll(en.mask);
-        const __amdgpu_buffer_rsrc_t wt = weight_tile(a.w_down, static_cast<int64_t>(en.expert) * a.k + row0, a.nbf);
+        const int64_t row = static_cast<int64_t>(en.expert) * a.k + row0;
+        const __amdgpu_buffer_rsrc_t wt[2] = {weight_tile(a.w_down, row, a.nbf), weight_tile(a.w_down, row + kTileRows, a.nbf)};
         for (int c0 = 0; c0 < count; c0 += kTokens) {
             ActOffsets<WORDS> ao[NT];
 #pragma unroll
@@ -404,17 +409,20 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
                     const int p = c0 + t * T::kTokens + i;
                     return p < count ? en.offset + p : -1;
                 });
-            double acc[NT][T::kVals];
+            double acc[2][NT][T::kVals];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int v = 0; v < T::kVals; ++v) acc[t][v] = 0.0;
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int v = 0; v < T::kVals; ++v) acc[w][t][v] = 0.0;
             struct {
-                Window w;
+                Window w[2];
                 Acts<WORDS> acts[NT];
             } ring[kAhead];
             auto load = [&](int p, int step) {
-                load_weights(wt, lane_off, step, step < min(st1, w_end), ring[p].w);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) load_weights(wt[w], lane_off, step, step < min(st1, w_end), ring[p].w[w]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if (c0 + t * T::kTokens < count) load_acts<WORDS>(words, scales, ao[t], step, step < st1, ring[p].acts[t]);
@@ -425,11 +433,15 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
             for (int s0 = st0; s0 < st1; s0 += kAhead) {
 #pragma unroll
                 for (int p = 0; p < kAhead; ++p) {
-                    Operands o;
-                    operands_of(ring[p].w, lane, o);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (c0 + t * T::kTokens < count) multiply<WORDS>(o, ring[p].acts[t], acc[t]);
+                    for (int w = 0; w < 2; ++w) {
+                        Operands o;
+                        operands_of(ring[p].w[w], lane, o);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            if (c0 + t * T::kTokens < count) multiply<WORDS>(o, ring[p].acts[t], acc[w][t]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                     load(p, s0 + p + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -439,9 +451,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
 #pragma unroll
                 for (int v = 0; v < T::kVals; ++v) {
                     const int p = c0 + t * T::kTokens + (lane >> 4) * T::kVals + v;
-                    if (p < count)
-                        mine[a.plan->pair_token[en.offset + p] * kTileRows + (lane & 15)] +=
-                            a.plan->pair_gate[en.offset + p] * (acc[t][v] * post);
+                    if (p >= count) continue;
+                    double *out = mine + a.plan->pair_token[en.offset + p] * kMoeDownRows + (lane & 15);
+                    const double gate = a.plan->pair_gate[en.offset + p];
+                    out[0] += gate * (acc[0][t][v] * post);
+                    out[kTileRows] += gate * (acc[1][t][v] * post);
                 }
         }
     }
@@ -449,9 +463,9 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
     double *parts = a.parts + static_cast<int64_t>(tile) * a.splits * outs;
     if (a.splits > 1) {
         // agent-scope stores, complete before this workgroup counts itself in
-        for (int i = threadIdx.x; i < outs; i += kThreads) {
+        for (int i = threadIdx.x; i < outs; i += kDownThreads) {
             double v = 0.0;
-            for (int w = 0; w < kWaves; ++w) v += sums[w * outs + i];
+            for (int w = 0; w < kDownWaves; ++w) v += sums[w * outs + i];
             __hip_atomic_store(parts + static_cast<int64_t>(split) * outs + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -465,15 +479,21 @@ __global__ __launch_bounds__(kThreads, NT == 1 && WORDS == 2 ? 4 : 2) void moe_d
         __syncthreads();
         if (!is_last) return;
     }
-    for (int i = threadIdx.x; i < outs; i += kThreads) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < outs; i += kDownThreads) {
         double v = 0.0;
         if (a.splits > 1) {
-            for (int s = 0; s < a.splits; ++s)
-                v += __hip_atomic_load(parts + static_cast<int64_t>(s) * outs + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            double part[kMoeMaxSplits];  // every load in flight at once
+#pragma unroll
+            for (int s = 0; s < kMoeMaxSplits; ++s)
+                part[s] = s < a.splits ? __hip_atomic_load(parts + static_cast<int64_t>(s) * outs + i, __ATOMIC_RELAXED,
+                                                           __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+#pragma unroll
+            for (int s = 0; s < kMoeMaxSplits; ++s) v += part[s];
         } else {
-            for (int w = 0; w < kWaves; ++w) v += sums[w * outs + i];
+            for (int w = 0; w < kDownWaves; ++w) v += sums[w * outs + i];
         }
-        const int64_t o = static_cast<int64_t>(i / kTileRows) * a.k + row0 + i % kTileRows;
+        const int64_t o = static_cast<int64_t>(i / kMoeDownRows) * a.k + row0 + i % kMoeDownRows;
         if (a.residual) v += static_cast<double>(a.residual[o]);
         a.y[o] = static_cast<float>(v);
     }
@@ -484,8 +504,8 @@ hipError_t run(const MoeArgs &a, hipStream_t stream) {
     const int most = std::min(a.experts, a.rows * a.top_k);
     moe_gate_up_mma_kernel<WORDS, NT><<<dim3(static_cast<unsigned>(most) * a.nbf), kGuThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    const size_t lds = static_cast<size_t>(kWaves) * a.rows * kTileRows * sizeof(double);
-    moe_down_mma_kernel<WORDS, NT><<<dim3(a.k / kTileRows * a.splits), kThreads, lds, stream>>>(a);
+    const size_t lds = static_cast<size_t>(kDownWaves) * a.rows * kMoeDownRows * sizeof(double);
+    moe_down_mma_kernel<WORDS, NT><<<dim3(a.k / kMoeDownRows * a.splits), kDownThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
