@@ -57,10 +57,10 @@ constexpr int kMaxWgLogits = 4096;  // logits of one workgroup of the maxima's k
 // Places the workspace's parts (base may be null: sizes only); returns its bytes.
 inline int64_t sample_layout(SampleArgs &a, uint8_t *base) {
     a.nsub = (a.n + kSubBlock - 1) / kSubBlock;
-    // Enough segments for two workgroups a CU, no more: each costs the row's
+    // Enough segments for a workgroup a CU (more do not fit), no more: each costs the row's
     // maximum, an empty histogram and the reading of its own by the last kernel.
     const int most = std::min(16, (a.n + kSegment - 1) / kSegment);
-    const int want = a.rows > 0 ? (512 + a.rows - 1) / a.rows : 1;
+    const int want = a.rows > 0 ? (256 + a.rows - 1) / a.rows : 1;
     a.segments = std::min(want, most);
     a.segment = ((a.n + a.segments - 1) / a.segments + kSegment - 1) / kSegment * kSegment;
     a.segments = (a.n + a.segment - 1) / a.segment;
