@@ -3,8 +3,9 @@ sampler.
 
 As in the package's other wrappers, argument marshalling only.  Every tensor of
 a call lives on one device, and the call runs on that device whichever is
-current, on ``stream`` or else on that device's current stream.  Outputs and
-workspaces that are not passed are allocated here.
+current, on ``stream`` (a torch stream or a raw handle) or else on that device's
+current stream.  Outputs and workspaces that are not passed are allocated here,
+and cleared where that is needed, on the same stream.
 """
 from __future__ import annotations
 
@@ -43,27 +44,14 @@ def _need(t, name: str, dtype, shape, device):
 _fns = {}
 
 
-def _call(fn: str, device, rows: int, stream, own, *args):
-    """Call a library function on `device` and `stream` (None: its current
-    stream).  `own`: tensors allocated here, which the caching allocator must
-    not hand out again before the stream is done with them."""
+def _call(fn: str, device, rows: int, *args):
+    """Call a library function on `device` and its current stream."""
     if rows == 0:
         return  # an empty tensor has no address; there is nothing to enqueue
-    if stream is None:
-        raw = _raw_stream(device.index)
-    elif hasattr(stream, "cuda_stream"):
-        raw = stream.cuda_stream
-        for t in own:
-            t.record_stream(stream)
-    else:
-        raw = int(stream)
-        if own:
-            ext = torch.cuda.ExternalStream(raw, device=device)
-            for t in own:
-                t.record_stream(ext)
     f = _fns.get(fn)
     if f is None:
         f = _fns[fn] = getattr(_q8.lib(), fn)
+    raw = _raw_stream(device.index)
     if _current_device() == device.index:
         status = f(*args, raw)
     else:
@@ -71,6 +59,22 @@ def _call(fn: str, device, rows: int, stream, own, *args):
             status = f(*args, raw)
     if status != 0:
         raise _q8.Q8Error(fn, status)
+
+
+def _on_stream(stream, device, fn, *args):
+    """fn(*args) with `stream` (a torch stream or a raw handle) current, so that what the
+    call allocates, and the workspace it clears, is ordered on that stream as well."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream must be one of {device}, not of {stream.device}")
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    for t in result if isinstance(result, tuple) else (result,):
+        t.record_stream(caller)  # where the caller, once it has waited, reads it
+    return result
 
 
 def _raw_stream(index: int) -> int:
@@ -143,31 +147,31 @@ def _rows(layer, x):
     return x.shape[0]
 
 
-def _work(layer, rows, workspace, own):
+def _work(layer, rows, workspace):
     if workspace is None:
-        workspace = layer.workspace(rows)
-        own.append(workspace)
-    elif workspace.dtype != _U8 or workspace.device != layer.device or not workspace.is_contiguous():
+        return layer.workspace(rows)
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != _U8 or workspace.device != layer.device or \
+            not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the layer's device")
     return workspace
 
 
-def _out(t, name, dtype, shape, layer, own):
+def _out(t, name, dtype, shape, layer):
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=layer.device)
-        own.append(t)
-    else:
-        _need(t, name, dtype, shape, layer.device)
+        return torch.empty(shape, dtype=dtype, device=layer.device)
+    _need(t, name, dtype, shape, layer.device)
     return t
 
 
 def moe_route(layer: MoeLayer, x: torch.Tensor, ids=None, gates=None, workspace=None, stream=None):
     """(ids int32, gates f32) [rows][top_k] that the layer's router chooses."""
-    rows, own = _rows(layer, x), []
-    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
-    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
-    workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe_route", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(), gates.data_ptr(),
+    if stream is not None:
+        return _on_stream(stream, layer.device, moe_route, layer, x, ids, gates, workspace)
+    rows = _rows(layer, x)
+    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer)
+    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer)
+    workspace = _work(layer, rows, workspace)
+    _call("q8_moe_route", layer.device, rows, layer._ref, x.data_ptr(), rows, ids.data_ptr(), gates.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return ids, gates
 
@@ -175,14 +179,16 @@ def moe_route(layer: MoeLayer, x: torch.Tensor, ids=None, gates=None, workspace=
 def moe_experts(layer: MoeLayer, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, residual=None, out=None,
                 workspace=None, stream=None) -> torch.Tensor:
     """y [rows][k] = residual + the gated sum of the given experts (ids outside the layer add nothing)."""
-    rows, own = _rows(layer, x), []
+    if stream is not None:
+        return _on_stream(stream, layer.device, moe_experts, layer, x, ids, gates, residual, out, workspace)
+    rows = _rows(layer, x)
     _need(ids, "ids", _I32, (rows, layer.top_k), layer.device)
     _need(gates, "gates", _F32, (rows, layer.top_k), layer.device)
     if residual is not None:
         _need(residual, "residual", _F32, (rows, layer.k), layer.device)
-    out = _out(out, "out", _F32, (rows, layer.k), layer, own)
-    workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe_experts", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows, ids.data_ptr(),
+    out = _out(out, "out", _F32, (rows, layer.k), layer)
+    workspace = _work(layer, rows, workspace)
+    _call("q8_moe_experts", layer.device, rows, layer._ref, x.data_ptr(), rows, ids.data_ptr(),
           gates.data_ptr(), _ptr(residual), out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
     return out
@@ -190,14 +196,16 @@ def moe_experts(layer: MoeLayer, x: torch.Tensor, ids: torch.Tensor, gates: torc
 
 def moe(layer: MoeLayer, x: torch.Tensor, residual=None, out=None, ids=None, gates=None, workspace=None, stream=None):
     """(y [rows][k], ids, gates): the whole layer, router and experts."""
-    rows, own = _rows(layer, x), []
+    if stream is not None:
+        return _on_stream(stream, layer.device, moe, layer, x, residual, out, ids, gates, workspace)
+    rows = _rows(layer, x)
     if residual is not None:
         _need(residual, "residual", _F32, (rows, layer.k), layer.device)
-    out = _out(out, "out", _F32, (rows, layer.k), layer, own)
-    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer, own)
-    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer, own)
-    workspace = _work(layer, rows, workspace, own)
-    _call("q8_moe", layer.device, rows, stream, own, layer._ref, x.data_ptr(), rows,
+    out = _out(out, "out", _F32, (rows, layer.k), layer)
+    ids = _out(ids, "ids", _I32, (rows, layer.top_k), layer)
+    gates = _out(gates, "gates", _F32, (rows, layer.top_k), layer)
+    workspace = _work(layer, rows, workspace)
+    _call("q8_moe", layer.device, rows, layer._ref, x.data_ptr(), rows,
           _ptr(residual), out.data_ptr(), ids.data_ptr(), gates.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return out, ids, gates
@@ -220,11 +228,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype != _F32 or not logits.is_cuda:
         raise ValueError("logits must be a f32 device tensor [rows][n]")
+    if stream is not None:
+        return _on_stream(stream, logits.device, sample, logits, u, temperature, top_k, top_p, min_p, idx, prob, workspace)
     rows, n = logits.shape
     if n > 1 and logits.stride(1) != 1:
         raise ValueError("logits must have unit stride within a row")
     ld = logits.stride(0) if rows > 1 else n
-    dev, own = logits.device, []
+    dev = logits.device
     for t, name, dtype in ((u, "u", _F32), (temperature, "temperature", _F32), (top_k, "top_k", _I32),
                            (top_p, "top_p", _F32), (min_p, "min_p", _F32), (idx, "idx", _I32), (prob, "prob", _F32)):
         if t is not None:
@@ -233,15 +243,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
         raise ValueError("u is required")
     if idx is None:
         idx = torch.empty(rows, dtype=_I32, device=dev)
-        own.append(idx)
     if prob is None:
         prob = torch.empty(rows, dtype=_F32, device=dev)
-        own.append(prob)
     if workspace is None:
         workspace = torch.empty(sample_workspace_bytes(rows, n), dtype=_U8, device=dev)
-        own.append(workspace)
-    elif workspace.dtype != _U8 or workspace.device != dev or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != _U8 or workspace.device != dev or \
+            not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-    _call("q8_sample", dev, rows, stream, own, logits.data_ptr(), ld, rows, n, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+    _call("q8_sample", dev, rows, logits.data_ptr(), ld, rows, n, _ptr(temperature), _ptr(top_k), _ptr(top_p),
           _ptr(min_p), u.data_ptr(), idx.data_ptr(), prob.data_ptr(), workspace.data_ptr(), workspace.numel())
     return idx, prob
