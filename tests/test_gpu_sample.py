@@ -182,3 +182,11 @@ def test_long_rows(rows, n):
     l = logits_of(rows, n, n)
     for kw in (dict(), dict(top_p=0.95), dict(top_k=1500, top_p=0.9), dict(top_k=100), dict(temperature=2.0, min_p=0.01)):
         check(l, what=kw, **kw)
+
+
+@pytest.mark.parametrize("kind", ["plain", "topp", "all", "minp", "wide"])
+@pytest.mark.parametrize("rows,n", [(40, 30011), (130, 9001), (256, 4100)])
+def test_rows_that_share_the_card(kind, rows, n):
+    """As many workgroups a row as the number of rows leaves."""
+    say("sample", kind, rows, n)
+    check(logits_of(rows, n, 77 + rows), what=kind, **KINDS[kind])
