@@ -35,8 +35,13 @@ namespace {
 constexpr double kUnit = 17592186044416.0;  // 2^44
 constexpr int kBins = kSampleBins;
 constexpr double kXLast = 31.191623125197536;  // 45 ln 2: weights are 0 beyond
-constexpr double kXRange = 31.25;              // of the histogram
-constexpr double kBinsPerX = kBins / kXRange;
+// Bins of the histogram over x = (m - l) / T: narrow ones up to 16, where the ends of the
+// prefixes are as good as always (of 2^19 equal tokens there the weight is 6 %), wider
+// ones behind.  With equal bins, 66 a unit, the tokens of a top-p's end and of the draw
+// could be more than one draw takes (152000 tokens, T = 1.4: 130 us a call, not 60).
+constexpr double kXFine = 16.0, kFinePerX = 112.0, kCoarsePerX = 16.75;
+constexpr double kFineBins = kXFine * kFinePerX;
+static_assert(kFineBins + (kXLast - kXFine) * kCoarsePerX < kBins - 1.5, "no token is in the last bin");
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kList = 4096;                 // tokens one sort takes
@@ -202,9 +207,16 @@ __device__ __forceinline__ u64 weight_within(double x) {
     const double v = __builtin_bit_cast(double, (static_cast<u64>(high) << 32) | static_cast<uint32_t>(bits));
     return __builtin_bit_cast(u64, v + 4503599627370496.0) & 0xfffffffffffffull;
 }
+// Where x is among the bins (bin b is around position b), and the x of a position.
+__device__ __forceinline__ double bin_position(double x) {
+    return fmin(x * kFinePerX, __builtin_fma(x, kCoarsePerX, kFineBins - kXFine * kCoarsePerX));
+}
+__device__ __forceinline__ double x_at(double position) {
+    return fmax(position / kFinePerX, kXFine + (position - kFineBins) / kCoarsePerX);
+}
 // The nearest bin's number, for 0 <= x <= kXLast.
 __device__ __forceinline__ int bin_within(double x) {
-    return static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(u64, __builtin_fma(x, kBinsPerX, 4503599627370496.0))));
+    return static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(u64, bin_position(x) + 4503599627370496.0)));
 }
 __device__ __forceinline__ u64 weight_of(double x) { return x <= kXLast ? weight_within(x) : 0; }
 // Bin of a token that can be drawn; kBins for the others.
@@ -331,17 +343,17 @@ __device__ __forceinline__ void for_tokens(Shared &s, const Row &r, const Subs &
     }
 }
 
-// A logit at or below every logit of bins 0 .. b: m - T (b + 1/2) / kBinsPerX, lowered
+// A logit at or below every logit of bins 0 .. b: m - T x of its lower edge, lowered
 // well past the rounding.  Infinite where that is no number.
 __device__ __forceinline__ float bin_floor(const Row &r, int b) {
-    const double m = static_cast<double>(r.m), down = (b + 0.5) / (kBinsPerX * r.rt);
+    const double m = static_cast<double>(r.m), down = x_at(b + 0.5) / r.rt;
     const float f = static_cast<float>(m - down - (1e-6 * (fabs(m) + down) + 1e-30));
     return f == f ? f : -__builtin_inff();
 }
 
 // Likewise at or above every logit of bins b and on.
 __device__ __forceinline__ float bin_ceil(const Row &r, int b) {
-    const double m = static_cast<double>(r.m), down = (b - 0.5) / (kBinsPerX * r.rt);
+    const double m = static_cast<double>(r.m), down = x_at(b - 0.5) / r.rt;
     const float f = static_cast<float>(m - down + (1e-6 * (fabs(m) + down) + 1e-30));
     return b > 0 && f == f ? f : __builtin_inff();
 }
@@ -861,7 +873,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
             last = static_cast<int>(s.pick_at);
         } else if (p.min_p < 1.f) {
             // tokens with exp(-x) >= min_p, and a bin more for the rounding of the bound
-            last = min(kBins - 1, static_cast<int>(-log(static_cast<double>(p.min_p)) * kBinsPerX) + 2);
+            last = min(kBins - 1, static_cast<int>(fmin(bin_position(-log(static_cast<double>(p.min_p))), kBins - 1.0)) + 2);
         } else {
             last = 0;
         }
@@ -907,7 +919,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
     // less than (1 - top_p) / e of the largest in all: the prefix ends before them.
     if (p.top_k == 0 && p.top_p < 1.f) {
         const double x = log(static_cast<double>(a.n) / (1.0 - static_cast<double>(fmaxf(p.top_p, 0.f)))) + 1.0;
-        tail = static_cast<int>(fmin(x * kBinsPerX + 2.0, kBins - 1.0));
+        tail = static_cast<int>(fmin(bin_position(x) + 2.0, kBins - 1.0));
     }
     const int i0 = whole ? 0 : segment * a.segment, i1 = whole ? a.n : min(a.n, i0 + a.segment);
     u64 strong = add_tokens(s, r, p, i0, i1, tail);
@@ -1065,7 +1077,7 @@ __global__ __launch_bounds__(kThreads) void sample_end_kernel(SampleArgs a) {
             sp.count = s.count[b] - sp.above_c;
         } else {
             // no counts are kept: a bound from the least weight a token of the bin has
-            const double least = static_cast<double>(weight_of((b + 1) / kBinsPerX)) * 0.999 - 1.0;
+            const double least = static_cast<double>(weight_of(x_at(b + 1.0))) * 0.999 - 1.0;
             const double most = least > 1.0 ? static_cast<double>(s.weight[b] - sp.above) / least + 1.0 : a.n;
             sp.count = most < a.n ? static_cast<uint32_t>(most) : static_cast<uint32_t>(a.n);
         }
