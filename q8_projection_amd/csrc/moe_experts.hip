@@ -23,10 +23,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int WORDS>
 constexpr int kRec = WORDS == 0 ? 128 : 32 * WORDS;
 constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves, at most
-// Gate and up: two workgroups a CU; one in the f32 mode, whose conversions need the
-// registers.  (Down: one, measured against two, which spilled: 37 against 50 us.)
-template <int WORDS>
-constexpr int kWavesPerSimd = WORDS == 0 ? 2 : 4;
+// Gate and up: two workgroups a CU.  (Down: one, measured against two, which spilled:
+// 37 against 50 us.)
+constexpr int kGateUpWaves = 4;  // of a SIMD
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), kBufferDword3);
@@ -152,7 +151,10 @@ template <int WORDS, int TG, typename S>
 __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t first_row, const ActSource &src,
                                              const int *tokens, int n, int lane, int wave) {
     constexpr int C = kChunk<WORDS>, R = kRec<WORDS>;
-    constexpr int kAhead = 4;  // windows in flight (3, 6 and 8 measured slower)
+    // windows in flight: 4 (3, 6 and 8 measured slower); in the f32 mode, whose conversions
+    // need the registers, 2 (8 tokens, 64 experts of which 8 are chosen: 81 us; 4: 92, one
+    // workgroup a CU and 4: 92)
+    constexpr int kAhead = WORDS == 0 ? 2 : 4;
     static_assert(C * R <= kThreads * 16 && C * TG <= kThreads, "a load a thread and token, a scale a thread");
     const int tid = threadIdx.x;
     double acc[TG];
@@ -218,7 +220,7 @@ __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t fir
 // block as quantize4 does, value for value.  MAX_TG: tokens a pass takes, at most;
 // ONE: one token in the call.
 template <int WORDS, int MAX_TG, bool ONE>
-__global__ __launch_bounds__(kThreads, kWavesPerSimd<WORDS>) void moe_gate_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kThreads, kGateUpWaves) void moe_gate_up_kernel(MoeArgs a) {
     __shared__ __align__(16) GateUpShared<WORDS, MAX_TG> s;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
