@@ -1,4 +1,24 @@
-// moe_experts.hip -- kernels and launchers described in moe_kernels.h.
+// moe_experts.hip -- the chosen experts' projections on vector instructions.
+//
+// Work split.  A wave streams a tile of 8 weight rows: lane 8 r + s takes row r
+// and blocks s, s + 8, .., so that one step of the wave reads 272 contiguous bytes
+// of each row, and the 8 lanes of a row meet at the end in three DPP adds (16 or 32
+// lanes a row were no faster).  The activations are read through LDS, where the
+// wave's 8 rows read the same addresses: staged once for the workgroup's eight
+// waves (gate and up, which share them) or in pieces of each wave's own (down,
+// whose waves have different experts).  One, two or four tokens a pass.
+//
+// Mathematics.  As in the GEMV: exact int32 block sums with v_dot4 (f64 products in
+// the f32 mode), block terms (d s) T added in f64; g, u and h are rounded to f32 once
+// each, as the projections' outputs are, and y once.
+//
+// Bound.  Reading the weights.  One token, two words: 8 experts of which 2 are chosen,
+// k 4096, ff 14336 (375 MB): gate/up 47 us (5.3 TB/s), down 25 us (5.0 TB/s); with 64
+// experts of which 8 are chosen, k 2048, ff 1408 (73 MB), 12 and 7.6 us, where the
+// start of the launches counts.  Eight tokens of the latter: 50 and 37 us (5.1 and
+// 3.4 TB/s).  The f32 mode is bound by its f64 products and conversions from four
+// tokens an expert on (32 tokens, 8 experts of which 2 are chosen, k 2048, ff 4096:
+// 146 and 101 us, of which the weights' reading is 28 and 14).
 #include <algorithm>
 
 #include "moe_kernels.h"

@@ -1,6 +1,13 @@
 // moe_plan.hip -- the first launch of the mixture-of-experts layer: the router's
 // logits, the activation quantization of x, the choice of experts and the plan
 // that groups the chosen (token, expert) pairs by expert.
+//
+// One launch for the four: the last workgroup of a group of tokens to finish its
+// logits makes their choices, the last of those the plan.  Launches of their own would
+// each add a start to a layer that takes 15 us at its smallest.  The logits are f64 sums rounded to f32 once, so
+// that the choice can be checked from them; gates are f64 quotients rounded once.
+// What bounds it is the chain of these steps, not the router's bytes: one token of 64
+// experts 6.8 us, 64 tokens 15 us (k 2048), given choices 3.8 us.
 #include "actquant.h"
 #include "device.h"
 #include "moe.h"
