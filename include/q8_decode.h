@@ -131,7 +131,8 @@ q8_status q8_sample(const float *logits, int64_t ld, int64_t rows, int64_t n, co
                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *idx,
                     float *prob, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Bytes of the q8_sample workspace (0 for sizes it refuses). */
+/* Bytes of the q8_sample workspace (0 for sizes it refuses).  They do not decrease
+ * with rows or n: a workspace for the largest call serves the smaller ones. */
 int64_t q8_sample_workspace_bytes(int64_t rows, int64_t n);
 
 #ifdef __cplusplus

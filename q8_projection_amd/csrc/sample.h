@@ -52,6 +52,10 @@ constexpr int kSampleBins = 2048;
 // and the sum of the weights that min-p keeps
 constexpr int kSampleSums = kSampleBins + kSampleBins / 2 + 1;
 constexpr int kSegment = 4096;  // logits one workgroup adds up, at least
+constexpr int kHistogramWgs = 256;  // workgroups that make histograms: one a CU
+// Workgroups that gather a call's rows, and logits one takes alone (64 mixed rows of 151936:
+// 29 us; with up to 512 workgroups 43, with 128 36)
+constexpr int kGatherWgs = 256, kGatherLogits = 65536;
 constexpr int kMaxWgLogits = 4096;  // logits of one workgroup of the maxima's kernel, 1024 a wave
 
 // Places the workspace's parts (base may be null: sizes only); returns its bytes.
@@ -60,7 +64,7 @@ inline int64_t sample_layout(SampleArgs &a, uint8_t *base) {
     // Enough segments for a workgroup a CU (more do not fit), no more: each costs the row's
     // maximum, an empty histogram and the reading of its own by the last kernel.
     const int most = std::min(16, (a.n + kSegment - 1) / kSegment);
-    const int want = a.rows > 0 ? (256 + a.rows - 1) / a.rows : 1;
+    const int want = a.rows > 0 ? (kHistogramWgs + a.rows - 1) / a.rows : 1;
     a.segments = std::min(want, most);
     a.segment = ((a.n + a.segments - 1) / a.segments + kSegment - 1) / kSegment * kSegment;
     a.segments = (a.n + a.segment - 1) / a.segment;
@@ -72,10 +76,13 @@ inline int64_t sample_layout(SampleArgs &a, uint8_t *base) {
         return p;
     };
     a.gathers = 1;
-    while (a.gathers < 8 && 2 * a.gathers * a.rows <= 256 && a.n / a.gathers > 65536) a.gathers *= 2;
+    while (a.gathers < 8 && 2 * a.gathers * a.rows <= kGatherWgs && a.n / a.gathers > kGatherLogits) a.gathers *= 2;
+    // Room for what any smaller call needs as well: the sizes grow with rows and n.
+    const int64_t histograms = std::min(int64_t(a.rows) * most, int64_t(a.rows) + kHistogramWgs);
+    const int64_t lists = a.n > kGatherLogits ? std::min(a.rows, kGatherWgs / 2) : 0;
     a.state = reinterpret_cast<RowState *>(take(sizeof(RowState) * int64_t(a.rows)));
-    a.sums = reinterpret_cast<unsigned long long *>(take(8 * kSampleSums * int64_t(a.rows) * a.segments));
-    a.near = reinterpret_cast<unsigned long long *>(take(a.gathers > 1 ? 8 * kNear * int64_t(a.rows) : 0));
+    a.sums = reinterpret_cast<unsigned long long *>(take(8 * kSampleSums * histograms));
+    a.near = reinterpret_cast<unsigned long long *>(take(8 * kNear * lists));
     a.submax = reinterpret_cast<float *>(take(int64_t(4) * a.rows * a.nsub));
     a.wavemax = reinterpret_cast<float *>(take(int64_t(4) * a.rows * a.nwave));
     return at;

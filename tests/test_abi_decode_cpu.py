@@ -130,3 +130,21 @@ def test_sample_refusals():
     for kw in (dict(idx=BASE + 4 * 3999), dict(prob=BASE), dict(idx=BASE + 20 * MB), dict(prob=BASE + 21 * MB + 12),
                dict(ws=BASE), dict(ws=BASE + 21 * MB), dict(idx=BASE + 17 * MB + 4)):
         assert sample(**kw) == ALIAS, kw
+
+
+def test_a_workspace_for_the_largest_call_serves_smaller_ones():
+    """The bytes do not decrease with any size, so that a loop keeps one workspace."""
+    lib = q8.lib()
+    rows = [0, 1, 2, 3, 15, 16, 17, 20, 31, 32, 33, 40, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 300, 1023, 1024, 1025, 5000]
+    ns = [1, 64, 65, 4096, 4097, 9000, 30000, 65536, 65537, 131072, 151936, 262144, (1 << 19) - 1]
+    for n in ns:
+        sizes = [lib.q8_sample_workspace_bytes(r, n) for r in rows]
+        assert sizes == sorted(sizes), n
+    for r in rows:
+        sizes = [lib.q8_sample_workspace_bytes(r, n) for n in ns]
+        assert sizes == sorted(sizes), r
+    for mode in (0, 1, 2):
+        for experts, top_k, k, ff in ((1, 1, 64, 64), (8, 2, 256, 128), (64, 8, 2048, 1408), (512, 16, 128, 64), (3, 2, 16448, 64)):
+            c = layer(mode=mode, experts=experts, top_k=top_k, k=k, ff=ff)
+            sizes = [lib.q8_moe_workspace_bytes(ctypes.addressof(c), r) for r in range(70)]
+            assert sizes[0] > 0 and sizes == sorted(sizes)
