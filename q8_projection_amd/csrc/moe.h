@@ -53,7 +53,7 @@ struct MoeArgs {
     int renormalize;
     int k, nbk;
     int ff, nbf;
-    int tiled;              // quantized activations in the matrix-core order (below)
+    int tiled;              // on the matrix cores, quantized activations in their order (below)
     int sbk, sbf;           // blocks of one row of xq and hq: nbk and nbf, rounded up to four if tiled
     int splits;             // workgroups that share a tile of the down projection
     // workspace
@@ -76,11 +76,12 @@ __host__ __device__ inline int record_offset(int tiled, int words, int blk, int 
                  : blk * (words * 32) + word * 32 + part * 4;
 }
 
-// Whether the experts run on the matrix cores: integer modes, for a mean of more than
-// two tokens an expert.  Both ways, vector and matrix, in us a layer (64 experts of which
-// 8 are chosen, k 2048, ff 1408; two words | one word): mean 1: 100, 100; mean 2: 144, 134 |
-// 132, 141; mean 3: 168, 148; mean 4: 204, 163 | 180, 159; mean 5: 237, 166; mean 6: | 224, 171.
-inline int moe_tiled(int words, const MoeArgs &a) { return words > 0 && a.rows * a.top_k > 2 * a.experts; }
+// Whether the experts run on the matrix cores: for a mean of more than two tokens an
+// expert, in the f32 mode more than three.  Both ways, vector and matrix, in us a layer (64
+// experts of which 8 are chosen, k 2048, ff 1408; two words | one word | f32): mean 1: 100, 100 |
+// | 161, 257; mean 2: 144, 134 | 132, 141 | 241, 335; mean 3: 168, 148; mean 4: 204, 163 |
+// 180, 159 | 386, 372; mean 5: 237, 166; mean 6: | 224, 171 | 535, 383; mean 8: | | 720, 389.
+inline int moe_tiled(int words, const MoeArgs &a) { return a.rows * a.top_k > (words ? 2 : 3) * a.experts; }
 
 // Output columns of a workgroup of the down projection on the matrix cores.
 constexpr int kMoeDownRows = 32;
@@ -109,8 +110,8 @@ inline int64_t moe_layout(MoeArgs &a, uint8_t *base, int words) {
     a.plan = reinterpret_cast<MoePlan *>(take(sizeof(MoePlan)));
     a.logits = reinterpret_cast<float *>(take(rows * a.experts * 4));
     a.tiled = moe_tiled(words, a);
-    a.sbk = a.tiled ? (a.nbk + 3) / 4 * 4 : a.nbk;
-    a.sbf = a.tiled ? (a.nbf + 3) / 4 * 4 : a.nbf;
+    a.sbk = a.tiled && words ? (a.nbk + 3) / 4 * 4 : a.nbk;
+    a.sbf = a.tiled && words ? (a.nbf + 3) / 4 * 4 : a.nbf;
     a.splits = moe_down_splits(a);
     a.xq = take(rows * a.sbk * words * 32);
     a.xs = reinterpret_cast<float *>(take(words ? rows * a.sbk * 4 : 0));

@@ -16,9 +16,8 @@
 // k 4096, ff 14336 (375 MB): gate/up 47 us (5.3 TB/s), down 25 us (5.0 TB/s); with 64
 // experts of which 8 are chosen, k 2048, ff 1408 (73 MB), 12 and 7.6 us, where the
 // start of the launches counts.  Eight tokens of the latter: 50 and 37 us (5.1 and
-// 3.4 TB/s).  The f32 mode is bound by its f64 products and conversions from four
-// tokens an expert on (32 tokens, 8 experts of which 2 are chosen, k 2048, ff 4096:
-// 146 and 101 us, of which the weights' reading is 28 and 14).
+// 3.4 TB/s).  The f32 mode is bound by its f64 products and conversions: 8 tokens of
+// the same 84 and 64 us.
 #include <algorithm>
 
 #include "moe_kernels.h"

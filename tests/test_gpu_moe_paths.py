@@ -39,8 +39,8 @@ def test_long_rows_and_columns(mode, rows, experts, top_k, k, ff):
     check(mode, rows, experts, top_k, k, ff)
 
 
-@pytest.mark.parametrize("mode", ["i8", "i8x2"])
-@pytest.mark.parametrize("rows,experts,top_k", [(4, 2, 1), (5, 2, 1), (8, 2, 1), (9, 2, 1), (3, 3, 2), (4, 3, 2), (6, 3, 2), (7, 3, 2), (10, 3, 2), (26, 3, 1), (64, 8, 1)])
+@pytest.mark.parametrize("mode", ["f32", "i8", "i8x2"])
+@pytest.mark.parametrize("rows,experts,top_k", [(4, 2, 1), (6, 2, 1), (7, 2, 1), (5, 2, 1), (8, 2, 1), (9, 2, 1), (3, 3, 2), (4, 3, 2), (6, 3, 2), (7, 3, 2), (10, 3, 2), (26, 3, 1), (64, 8, 1)])
 def test_number_of_tokens_an_expert(mode, rows, experts, top_k):
     check(mode, rows, experts, top_k, 320, 192)
 
