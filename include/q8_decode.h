@@ -35,7 +35,9 @@ extern "C" {
  * where a and a' are x and h in the layer's activation mode: quantized as
  * q8_quantize_act does (integer modes) or as they are (Q8_ACT_F32).  A layer is
  * for a few tokens: what it costs is reading each chosen expert's weights from
- * memory once per slice of 64 rows; unchosen experts are not read.
+ * memory once per slice of 64 rows; unchosen experts are not read.  The same call
+ * gives the same bits every time; between batches a token's y can differ by the order
+ * of its f64 sums (a step of the f32 result), since their number decides the kernels.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t mode;        /* q8_act_mode of the three projections */
