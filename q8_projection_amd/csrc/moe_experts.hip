@@ -218,7 +218,8 @@ __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t fir
         for (int s0 = 0; s0 < steps; s0 += kAhead) {
 #pragma unroll
             for (int p = 0; p < kAhead; ++p) {
-                // a dead step's windows are zeros; its activations are read from the chunk
+                // a dead step's windows are zeros, and so is what the chunk holds behind its blocks
+                static_assert(C / kStepBlocks % kAhead == 0, "dead steps stay in the chunk");
                 const int at = min(s0 + p, C / kStepBlocks - 1);
                 compute<WORDS, TG, C * R, C>(ring[p], rec + at * (kStepBlocks * R), scale + at * kStepBlocks, lane, acc);
                 wt.next(ring[p]);
@@ -316,9 +317,12 @@ __device__ __forceinline__ void down_pass(uint8_t *buf, float *sbuf, const uint8
     for (int t = 0; t < TG; ++t) acc[t] = 0.0;
     uint4 v[TG][kLoads];
     float sc = 0.f;
+    // zeros from st1 on: the ring's last steps have zero weights, and an infinite h there,
+    // which is another wave's to add, would make the wave's sum NaN
+    const int end = min(st1 * kStepBlocks, src.nb);
     auto load = [&](int st) {  // the segment that begins at step st
         const int b0 = st * kStepBlocks;
-        const int nblk = st < st1 ? min(kSegBlocks, src.nb - b0) : 0;
+        const int nblk = min(kSegBlocks, end - b0);
 #pragma unroll
         for (int t = 0; t < TG; ++t)
 #pragma unroll
