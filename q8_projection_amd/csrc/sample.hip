@@ -132,7 +132,7 @@ __device__ __forceinline__ Params params_of(const SampleArgs &a, int row) {
     p.u = a.u[row];
     p.greedy = !(p.t > 0.0f);
     p.by_k = p.top_k > 0 && p.top_k <= min(kQuickTopK, a.nsub);
-    p.by_p = p.top_k == 0 && !(p.top_p < 1.f) && p.min_p > 0.f;
+    p.by_p = !p.greedy && p.top_k == 0 && !(p.top_p < 1.f) && p.min_p > 0.f;
     return p;
 }
 
