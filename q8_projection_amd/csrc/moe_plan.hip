@@ -20,8 +20,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-static_assert(kMoeCounterBytes / 4 / kMoeCounterStride > kMoeSlice / 4, "a counter for each token group and one more");
 constexpr int kTokenGroup = 4;  // tokens one workgroup dots a router row with, and then a wave each chooses for
+static_assert((kMoeSlice / kTokenGroup + 1) * kMoeCounterStride <= kMoeTileCounter,
+              "a counter for each token group and one more, before the tiles' counters");
 
 // z[t][e] for one expert and up to 4 tokens, by one workgroup: threads stride over k
 // four values at a time (every product exact in f64, 24 x 24 bits, and every sum in
