@@ -148,8 +148,10 @@ __global__ __launch_bounds__(kMaxThreads) void sample_max_kernel(SampleArgs a) {
     float most = -__builtin_inff();
 #pragma unroll
     for (int p = 0; p < kMaxPerThread; ++p) {
-        f[p].trim();  // NaN loses every comparison of fmaxf
-        const float v = row_max(fmaxf(fmaxf(f[p].v[0], f[p].v[1]), fmaxf(f[p].v[2], f[p].v[3])));
+        f[p].trim();
+        // fmaxf passes a signaling NaN on and drops a quiet one: the sums are quiet, so that NaN
+        // loses every comparison
+        const float v = row_max(fmaxf(fmaxf(f[p].v[0] + 0.0f, f[p].v[1] + 0.0f), fmaxf(f[p].v[2] + 0.0f, f[p].v[3] + 0.0f)));
         most = fmaxf(most, v);
         const int sub = (q0 + p * kMaxThreads) / 16;
         if ((threadIdx.x & 15) == 0 && sub < a.nsub) a.submax[static_cast<int64_t>(blockIdx.x) * a.nsub + sub] = v;
@@ -453,7 +455,7 @@ struct EndTest {
 
 __device__ __forceinline__ End find_end(Shared &s, const Row &r, const Subs &subs, Span sp, const EndTest &cond) {
     const auto want = [&](float sub) { return sub >= sp.llo && bin_of(x_of(r, sub)) <= sp.bin; };
-    const auto some = [&](const float *v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= sp.llo; };
+    const auto some = [&](const float *v) { return v[0] >= sp.llo || v[1] >= sp.llo || v[2] >= sp.llo || v[3] >= sp.llo; };
     while (true) {
         if (sp.count <= kList) {
             // gather, sort in descending (key, -index), scan
