@@ -35,7 +35,6 @@ constexpr int kHBlock = 32;  // h values of one workgroup of the gate/up kernel:
 constexpr uint32_t kBufferDword3 = 0x00020000u;
 constexpr uint32_t kOob = 0x80000000u;  // an offset past every range: loads there read zeros
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Bytes of a record: one block's words (f32 mode: its 32 values).
