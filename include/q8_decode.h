@@ -33,11 +33,24 @@ extern "C" {
  *                                     every product and sum in f64, rounded once
  *
  * where a and a' are x and h in the layer's activation mode: quantized as
- * q8_quantize_act does (integer modes) or as they are (Q8_ACT_F32).  A layer is
- * for a few tokens: what it costs is reading each chosen expert's weights from
- * memory once per slice of 64 rows; unchosen experts are not read.  The same call
- * gives the same bits every time; between batches a token's y can differ by the order
- * of its f64 sums (a step of the f32 result), since their number decides the kernels.
+ * q8_quantize_act does (integer modes) or as they are (Q8_ACT_F32).  Finite inputs
+ * may give an h that overflows f32: in Q8_ACT_F32 y is then the formula's with an
+ * infinite h; in the integer modes that token's y is unspecified.
+ *
+ * A layer is for a few tokens: what it costs is reading the chosen experts' weights
+ * (unchosen experts are not read).  Rows go in slices of 64, one after the other, each
+ * of which reads its experts' weights again.  Within a slice a pass over an expert's
+ * weights serves 4 of its tokens if the slice's rows * top_k is at most 2 * n_experts
+ * (3 * n_experts in Q8_ACT_F32), else 16 in Q8_ACT_F32, 16 or 32 in Q8_ACT_I8 and 8 or 16 in Q8_ACT_I8X2; an expert
+ * with more tokens takes several passes, which the caches serve as far as they hold it.
+ *
+ * The same call gives the same bits every time.  The number of rows, and what the other
+ * rows choose, decide the kernels and the order of the f64 sums: between batches a
+ * token's g, u, h or y can round to the neighbouring f32, and in the integer modes a
+ * quantized value of h can then differ by one.
+ *
+ * Limits (else Q8_E_SHAPE): those of the fields below, 0 <= rows <= 2^20, and at most
+ * 2^31 blocks in each of the three matrices.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t mode;        /* q8_act_mode of the three projections */
@@ -126,7 +139,8 @@ q8_status q8_moe(const q8_moe_layer *layer, const float *x, int64_t rows, const 
  *                 which need not be cleared.  Calls in flight at once must not
  *                 share one.
  * All arrays 4-byte aligned; the outputs and the workspace must not overlap any
- * other argument.  Limits (else Q8_E_SHAPE): 1 <= n < 2^19, 0 <= rows <= 65536.
+ * other argument.  Limits (else Q8_E_SHAPE): 1 <= n < 2^19, 0 <= rows <= 65536,
+ * ld <= 2^40.
  * Errors: Q8_E_NULL, Q8_E_SHAPE, Q8_E_ALIGN, Q8_E_ALIAS, Q8_E_HIP.
  * ------------------------------------------------------------------------- */
 q8_status q8_sample(const float *logits, int64_t ld, int64_t rows, int64_t n, const float *temperature,
