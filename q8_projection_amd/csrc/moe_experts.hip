@@ -41,8 +41,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int WORDS>
 constexpr int kRec = WORDS == 0 ? 128 : 32 * WORDS;
 constexpr int kTokenGroup = 4;  // tokens one pass over a tile serves, at most
-// Gate and up: two workgroups a CU.  (Down: one, measured against two, which spilled:
-// 37 against 50 us.)
+// Gate and up: two workgroups a CU.  In the f32 mode with four tokens a pass that cap on
+// registers spills three of them (16 bytes a lane), and is faster all the same (81 against
+// 92 us, below).  (Down: one, measured against two, which spilled more: 37 against 50 us.)
 constexpr int kGateUpWaves = 4;  // of a SIMD
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {

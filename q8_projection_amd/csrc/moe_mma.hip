@@ -23,8 +23,11 @@
 // and h are rounded to f32 once each, as the projections' outputs are, and y once.
 //
 // Bound.  Reading the weights: 64 tokens, 64 experts of which 8 are chosen, k 2048, ff 1408
-// (590 MB): gate/up 100 us (3.9 TB/s, the rate of a long read), down 69 us (2.8 TB/s).
-// The arithmetic is hidden behind it: without the products each is 1 to 3 us faster.
+// (590 MB): gate/up 100 us (3.9 TB/s), down 69 us (2.8 TB/s), where the vector kernels read
+// one token's large experts at 5.3 and 5.0.  The products are hidden behind the loads
+// (without them each is 1 to 3 us faster); what is not is each workgroup's beginning and
+// end: gate/up stages up to 66 KB of activations for 8 steps a wave and then joins and
+// quantizes 32 values of h a token.
 // The f32 mode is bound by its f64 instructions and the conversions beside them: 38
 // tokens, 22 experts of which 8 are chosen, k 1408, ff 5184 (13.3 GFLOP, of which 16-token tiles
 // make 17): gate/up 275 us, down 219 us.
@@ -67,7 +70,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint3
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), kBufferDword3);
 }
 
-// 16 rows of one expert's matrix (fewer at its end: `rows`).
+// 16 rows of one expert's matrix (k and ff are multiples of 64: whole tiles).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t weight_tile(const uint8_t *w, int64_t first_row, int nb) {
     const uint32_t row_bytes = static_cast<uint32_t>(nb) * kBlockBytes;
     return buffer_of(w + first_row * row_bytes, kTileRows * row_bytes);

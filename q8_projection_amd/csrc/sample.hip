@@ -26,10 +26,14 @@
 //    sorts just those bins' tokens.
 // A row is read from memory once; the caches serve what is read again.
 //
-// Bound.  The chain of dependent steps, and with many rows the arithmetic on each token
-// (some 35 instructions, most of them f64, for a histogram; 16 for a gather): one row
-// of 151936 with top-k 3 + 10 + 2 us; 8 rows of 32003 with top-p 3 + 11 + 18 us; 64 rows of
-// 151936, each kind of filter, 8 + 23 + 29 us (39 MB); 256 rows of 50257 8 + 28 + 20 us (51 MB).
+// Bound.  The chain of dependent steps, and with many rows one workgroup's share of a row:
+// one row of 151936 with top-k 3 + 10 + 2 us; 8 rows of 32003 with top-p 3 + 11 + 18 us; 64
+// rows of 151936, each kind of filter, 8 + 22 + 30 us (39 MB), all with top-p 8 + 24 + 35; 256
+// rows of 50257, min-p on half, 9 + 28 + 21 us (51 MB), all plain 8 + 24 + 24.  The histogram
+// of 64 rows takes as long for 24 rows of them as for all: workgroups are dealt by the
+// number of rows, so 96 and 128 of 256 CUs work in the first of each pair, and what counts is
+// the time of one workgroup (41000 and 50000 logits; some 35 instructions each, most of
+// them f64, are 9 and 11 us of a CU, the rest is latency).
 #include "device.h"
 #include "sample.h"
 
