@@ -21,6 +21,7 @@ def test_the_largest_logit_of_a_row_with_filters_set(rows, n):
             assert (idx == n // 3).all() and (prob == np.float32(1)).all()
 
 
+@pytest.mark.filterwarnings("ignore:invalid value encountered in cast")
 def test_signaling_nan_is_no_candidate_either():
     l = logits_of(4, 5003, 43)
     bits = l.view(np.uint32)
