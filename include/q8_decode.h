@@ -41,8 +41,9 @@ extern "C" {
  * (unchosen experts are not read).  Rows go in slices of 64, one after the other, each
  * of which reads its experts' weights again.  Within a slice a pass over an expert's
  * weights serves 4 of its tokens if the slice's rows * top_k is at most 2 * n_experts
- * (3 * n_experts in Q8_ACT_F32), else 16 in Q8_ACT_F32, 16 or 32 in Q8_ACT_I8 and 8 or 16 in Q8_ACT_I8X2; an expert
- * with more tokens takes several passes, which the caches serve as far as they hold it.
+ * (3 * n_experts in Q8_ACT_F32), else 16 in Q8_ACT_F32, 16 or 32 in Q8_ACT_I8 and 8 or
+ * 16 in Q8_ACT_I8X2; an expert with more tokens takes several passes, which the caches
+ * serve as far as they hold it.
  *
  * The same call gives the same bits every time.  The number of rows, and what the other
  * rows choose, decide the kernels and the order of the f64 sums: between batches a

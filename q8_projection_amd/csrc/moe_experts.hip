@@ -218,7 +218,8 @@ __device__ __forceinline__ void gate_up_pass(S &s, const uint8_t *w, int64_t fir
         for (int s0 = 0; s0 < steps; s0 += kAhead) {
 #pragma unroll
             for (int p = 0; p < kAhead; ++p) {
-                // a dead step's windows are zeros, and so is what the chunk holds behind its blocks
+                // a dead step's windows are zeros, and so is what the chunk holds behind its blocks.  (The
+                // min changes no index; without it one token of large experts took 79.7 us, not 77.7.)
                 static_assert(C / kStepBlocks % kAhead == 0, "dead steps stay in the chunk");
                 const int at = min(s0 + p, C / kStepBlocks - 1);
                 compute<WORDS, TG, C * R, C>(ring[p], rec + at * (kStepBlocks * R), scale + at * kStepBlocks, lane, acc);
