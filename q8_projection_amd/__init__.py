@@ -6,7 +6,8 @@ allocated here with ``torch.empty`` when the caller passes none.  The names and
 arguments mirror the C ABI in ``include/q8.h``; see there for layouts,
 numerics and errors.  The steps of a decode step around the projections (the
 mixture-of-experts layer, the sampler; ``include/q8_decode.h``) are in
-``decode.py`` and re-exported here.
+``decode.py``, the key/value cache and its attention (``include/q8_cache.h``) in
+``cache.py``; both are re-exported here.
 
 The library must be built (``python q8_projection_amd/build.py``); importing
 this module without it, or calling a projection without a GPU, raises.
@@ -53,6 +54,12 @@ SIGNATURES = {
     "q8_moe": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
     "q8_sample": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "q8_sample_workspace_bytes": (_I64, [_I64, _I64]),
+    # include/q8_cache.h
+    "q8_cache_page_bytes": (_I64, [_P]),
+    "q8_cache_append": (_I, [_P, _P, _P, _I64, _P, _I64, _P]),
+    "q8_cache_read": (_I, [_P, _P, _P, _P, _P]),
+    "q8_attention": (_I, [_P, _P, _P, _I64, _I64, ctypes.c_float, _I64, _P, _P, _P, _I64, _P]),
+    "q8_attention_workspace_bytes": (_I64, [_P, _P, _I64]),
 }
 
 _lib = None
@@ -326,3 +333,5 @@ def block_sums(mode, w: torch.Tensor, n: int, k: int, hi, lo=None, out=None, row
 
 
 from .decode import MoeLayer, moe, moe_experts, moe_route, moe_workspace_bytes, sample, sample_workspace_bytes  # noqa: E402
+from .cache import (CacheBatch, KVCache, attention, attention_workspace, attention_workspace_bytes, cache_append,  # noqa: E402
+                    cache_page_bytes, cache_read)

@@ -1,0 +1,331 @@
+// cache.hip -- keys and values quantized as they are written into a paged cache,
+// and read back (q8_cache.h has the formulas and the layout).
+//
+// One wave serves a 32-token tile of one sequence and 64 dimensions of one kv head.
+// Both kernels move each f32 value and each code once and are bound by that and, for
+// a few tokens, by one wave's chain of load, reduction and store.  A tile belongs to
+// one wave because two tokens share a byte of the 4-bit value codes: the wave that
+// writes the byte has both tokens, so that no atomics are needed.
+//   keys  : lane = 8 tokens x 8 dimensions: a block's 32 values lie in 4 lanes, whose
+//           smallest and largest meet in two DPP steps.
+//   values: lane (g, c) = tokens 8 g .. 8 g + 7 of dimensions 16 w + c, w = 0 .. 3: the
+//           lane holds all eight tokens of its dwords, and a block's values lie in the
+//           16 lanes of a DPP row.
+#include <algorithm>
+
+#include "cache.h"
+#include "device.h"
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// The format's constants: the scale keeps 23 - kDrop mantissa bits.
+template <int BITS>
+struct Format {
+    static constexpr int kDrop = BITS == 4 ? 18 : 20;
+    static constexpr float kSteps = BITS == 4 ? 15.0f : 127.0f;
+    static constexpr float kTop = BITS == 4 ? 4352.0f : 512.0f;
+    static constexpr float kLowest = BITS == 4 ? 0x1p-19f : 0x1p-17f;  // the smallest scale
+};
+
+// high - low, rounded up where it rounds: a span just over kSteps d must not pass for kSteps d.
+__device__ __forceinline__ float span_of(float low, float high) {
+    const float s = high - low, t = s - high;
+    const float rest = (high - (s - t)) - (low + t);  // the exact difference's other part
+    return rest > 0.0f ? __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, s) + 1u) : s;
+}
+
+// The smallest scale d of the format with kSteps d >= span.  span / kSteps is off by less
+// than half a step of f32, and no quotient of an f32 by 15 or 127 rounds to a scale of at most
+// 6 bits without being that scale (it would lie nearer to it than the products' common grid
+// allows), so rounding the quotient up on the scales' grid is exact.
+template <int BITS>
+__device__ __forceinline__ float scale_of(float span) {
+    using F = Format<BITS>;
+    const float t = fminf(span / F::kSteps, F::kTop);
+    constexpr uint32_t step = (1u << F::kDrop) - 1;
+    const float up = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, t) + step) & ~step);
+    const float low = ceilf(t * (1.0f / F::kLowest)) * F::kLowest;  // binary16's subnormal grid
+    return t < 0x1p-14f ? low : up;
+}
+
+// rint(x / d), with r = 1 / d correctly rounded.  The first correction of x * r, which is up to
+// one and a half steps off, leaves one of the two neighbours of x / d, the second the correctly
+// rounded quotient (Markstein's theorem), and that is a half-integer only if the exact one is (x
+// has 24 bits, d six).  One correction alone rounds some quotients next to a half-integer wrongly.
+__device__ __forceinline__ float steps_of(float x, float d, float r) {
+    float q = x * r;
+    q = __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
+    return rintf(__builtin_fmaf(__builtin_fmaf(-q, d, x), r, q));
+}
+
+__device__ __forceinline__ float row_min(float v) {
+    v = fminf(v, dpp_f32<0xb1>(v));      // quad_perm [1,0,3,2]
+    v = fminf(v, dpp_f32<0x4e>(v));      // quad_perm [2,3,0,1]
+    v = fminf(v, dpp_f32<0x141>(v));     // row_half_mirror
+    return fminf(v, dpp_f32<0x140>(v));  // row_mirror
+}
+
+__device__ __forceinline__ uint32_t half_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+
+// A block's scale, its reciprocal, its zero point (4 bits) and its word.
+template <int BITS>
+struct Block {
+    float d, r, z;
+
+    // low, high: the block's smallest value or 0, its largest or 0
+    __device__ __forceinline__ void set(float low, float high) {
+        d = scale_of<BITS>(BITS == 4 ? span_of(low, high) : fmaxf(high, -low));
+        r = d > 0 ? 1.0f / d : 0.0f;
+        z = BITS == 4 ? fminf(steps_of(-low, d, r), 15.0f) : 0.0f;
+    }
+    __device__ __forceinline__ uint32_t word() const {
+        return half_bits(d) | (BITS == 4 ? static_cast<uint32_t>(z) : 0u);
+    }
+    __device__ __forceinline__ uint32_t code(float x) const {
+        const float n = steps_of(x, d, r);
+        if (BITS == 4) return static_cast<uint32_t>(fminf(fmaxf(n + z, 0.0f), 15.0f));
+        return static_cast<uint32_t>(fminf(fmaxf(n, -127.0f), 127.0f) + 128.0f);
+    }
+};
+
+// What a wave serves: a tile of a sequence, 64 dimensions of a kv head.
+struct Work {
+    int s, tile, head, part;
+};
+
+template <int D>
+__device__ __forceinline__ Work work_of(const CacheArgs &c, int tiles) {
+    constexpr int kParts = D / 64;
+    const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * kWaves;
+    const int per = c.kv_heads * kParts;
+    const int64_t rest = wave / per;
+    const int u = static_cast<int>(wave - rest * per);
+    Work w;
+    w.s = static_cast<int>(rest / tiles);
+    w.tile = static_cast<int>(rest % tiles);
+    w.head = u / kParts;
+    w.part = u % kParts;
+    return w;
+}
+
+// Tiles that the rows of one sequence can lie in: `rows` tokens anywhere.
+inline int64_t tiles_of(int rows) { return (int64_t(rows) + kTileTokens - 2) / kTileTokens + 1; }
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int tiles) {
+    using T = Tile<BITS, D>;
+    const Work w = work_of<D>(a.c, tiles);
+    if (w.s >= a.c.sequences) return;
+    const Rows rows = sequence_rows(a.c, w.s);
+    const int t = max(rows.at, 0) / kTileTokens + w.tile;  // tile of the sequence
+    const int t0 = t * kTileTokens;
+    // tokens [lo, hi) of the tile are written
+    const int lo = max(rows.at - t0, 0), hi = min(min(rows.at + rows.n, rows.end) - t0, kTileTokens);
+    if (lo >= hi) return;
+    uint8_t *tile = tile_at<BITS, D>(a.c, w.s, t, w.head);
+    if (!tile) return;
+    const int lane = threadIdx.x & 63;
+    const int row0 = rows.first + (t0 - rows.at);  // row of the tile's token 0
+    const int dim0 = w.part * 64;
+    const int64_t column = int64_t(w.head) * D + dim0;
+
+    // Loads first.  A token that is not written loads the nearest one that is.
+    const int sub = lane >> 3, j = lane & 7;
+    float kx[4][8];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int tok = min(max(p * 8 + sub, lo), hi - 1);
+        const float *src = a.k + (row0 + tok) * a.k_ld + column + j * 8;
+        const float4 x = *reinterpret_cast<const float4 *>(src), y = *reinterpret_cast<const float4 *>(src + 4);
+        kx[p][0] = x.x, kx[p][1] = x.y, kx[p][2] = x.z, kx[p][3] = x.w;
+        kx[p][4] = y.x, kx[p][5] = y.y, kx[p][6] = y.z, kx[p][7] = y.w;
+    }
+    const int g = lane >> 4, c = lane & 15;
+    float vx[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int tok = min(max(g * 8 + n, lo), hi - 1);
+        const float *src = a.v + (row0 + tok) * a.v_ld + column + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vx[n][i] = src[16 * i];
+    }
+
+    // Keys: a pass is 8 tokens.
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float low = 0.0f, high = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) low = fminf(low, kx[p][e]), high = fmaxf(high, kx[p][e]);
+        low = fminf(low, dpp_f32<0xb1>(low)), high = fmaxf(high, dpp_f32<0xb1>(high));
+        low = fminf(low, dpp_f32<0x4e>(low)), high = fmaxf(high, dpp_f32<0x4e>(high));
+        Block<BITS> b;
+        b.set(low, high);
+        uint32_t code[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) code[BITS == 4 ? 0 : e / 4] |= b.code(kx[p][e]) << (BITS == 4 ? 4 * e : 8 * (e % 4));
+        const int tok = p * 8 + sub;
+        if (tok < lo || tok >= hi) continue;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(tile + tok * T::kRow + (dim0 + j * 8) * BITS / 8);
+        dst[0] = code[0];
+        if (BITS == 8) dst[1] = code[1];
+        if (j % 4 == 0)
+            reinterpret_cast<uint16_t *>(tile + T::kKeyWords)[key_word(tok, dim0 / 32 + j / 4, T::kBlocks)] =
+                static_cast<uint16_t>(b.word());
+    }
+
+    // Values: the eight tokens of dimensions 16 i + c.
+    uint32_t code[4][2] = {};
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int tok = g * 8 + n;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // block
+            const float low = row_min(fminf(fminf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
+            const float high = row_max(fmaxf(fmaxf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
+            Block<BITS> b;
+            b.set(low, high);
+#pragma unroll
+            for (int i = 2 * u; i < 2 * u + 2; ++i) {
+                const uint32_t q = b.code(vx[n][i]);
+                // 8 bits: byte 2 (n % 4) + n / 4
+                if (BITS == 4) code[i][0] |= q << (4 * n);
+                else code[i][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
+            }
+            if (c == n && tok >= lo && tok < hi)
+                reinterpret_cast<uint16_t *>(tile + T::kValueWords)[value_word(tok, dim0 / 32 + u)] =
+                    static_cast<uint16_t>(b.word());
+        }
+    }
+    // the lane's tokens that are written, and what it keeps of those that are not
+    const int first = max(lo - g * 8, 0), last = min(hi - g * 8, 8);
+    if (first >= last) return;
+    uint32_t keep[2] = {0, 0};
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        if (n >= first && n < last) continue;
+        if (BITS == 4) keep[0] |= 0xfu << (4 * n);
+        else keep[(n & 3) >> 1] |= 0xffu << (16 * (n & 1) + 8 * (n >> 2));
+    }
+    constexpr int kWords = BITS / 4;  // dwords of a dimension
+    uint32_t *dst = reinterpret_cast<uint32_t *>(tile + T::kValues) + ((w.part * kWords * 4 + g) * 16 + c) * 4;
+#pragma unroll
+    for (int h = 0; h < kWords; ++h) {  // 16 bytes a lane: 4 dimensions of 4 bits, 2 of 8
+        uint4 *at = reinterpret_cast<uint4 *>(dst + h * 4 * 16 * 4);
+        uint4 out;
+        if (BITS == 4) out = make_uint4(code[0][0], code[1][0], code[2][0], code[3][0]);
+        else out = make_uint4(code[2 * h][0], code[2 * h][1], code[2 * h + 1][0], code[2 * h + 1][1]);
+        const uint32_t k0 = keep[0], k1 = BITS == 4 ? k0 : keep[1];
+        if (k0 | k1) {
+            const uint4 old = *at;
+            out.x = (out.x & ~k0) | (old.x & k0);
+            out.y = (out.y & ~k1) | (old.y & k1);
+            out.z = (out.z & ~k0) | (old.z & k0);
+            out.w = (out.w & ~k1) | (old.w & k1);
+        }
+        *at = out;
+    }
+}
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int tiles) {
+    using T = Tile<BITS, D>;
+    const Work w = work_of<D>(a.c, tiles);
+    if (w.s >= a.c.sequences) return;
+    const Rows rows = sequence_rows(a.c, w.s);
+    // the first row's token may lie before the sequence: its tile is then a negative one
+    const int t = (rows.at >> 5) + w.tile, t0 = t * kTileTokens;
+    const int lo = max(rows.at - t0, 0), hi = min(rows.at + rows.n - t0, kTileTokens);  // rows of the call
+    if (lo >= hi) return;
+    const int have = rows.end - t0;  // tokens from here on are none
+    const uint8_t *tile = t < 0 || have <= 0 ? nullptr : tile_at<BITS, D>(a.c, w.s, t, w.head);
+    const int lane = threadIdx.x & 63, dim0 = w.part * 64;
+    const int64_t ld = int64_t(a.c.kv_heads) * D;
+    const int64_t origin = (rows.first + (t0 - rows.at)) * ld + int64_t(w.head) * D + dim0;  // token 0's
+
+    const int sub = lane >> 3, j = lane & 7;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int tok = p * 8 + sub;
+        if (tok < lo || tok >= hi) continue;
+        float x[8] = {};
+        if (tile && tok < have) {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(tile + tok * T::kRow + (dim0 + j * 8) * BITS / 8);
+            const uint32_t code[2] = {src[0], BITS == 8 ? src[1] : 0};
+            const uint32_t word = reinterpret_cast<const uint16_t *>(tile + T::kKeyWords)[key_word(tok, dim0 / 32 + j / 4, T::kBlocks)];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = value_of<BITS>(word, BITS == 4 ? code[0] >> (4 * e) & 15u : code[e / 4] >> (8 * (e % 4)) & 255u);
+        }
+        float *dst = a.k + origin + tok * ld + j * 8;
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+
+    const int g = lane >> 4, c = lane & 15;
+    constexpr int kWords = BITS / 4;
+    uint32_t code[kWords * 4] = {}, word[2][4] = {};
+    if (tile) {
+#pragma unroll
+        for (int h = 0; h < kWords; ++h) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(tile + T::kValues +
+                                                            (((w.part * kWords + h) * 4 + g) * 16 + c) * 16);
+            code[4 * h] = x.x, code[4 * h + 1] = x.y, code[4 * h + 2] = x.z, code[4 * h + 3] = x.w;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(tile + T::kValueWords + ((dim0 / 32 + u) * 4 + g) * 16);
+            word[u][0] = x.x, word[u][1] = x.y, word[u][2] = x.z, word[u][3] = x.w;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int tok = g * 8 + n;
+        if (tok < lo || tok >= hi) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // words lie in pairs of tokens n, n + 4
+            const uint32_t m = word[i >> 1][n & 3] >> (16 * (n >> 2)) & 0xffffu;
+            const uint32_t q = BITS == 4 ? code[i] >> (4 * n) & 15u
+                                         : code[2 * i + ((n & 3) >> 1)] >> (16 * (n & 1) + 8 * (n >> 2)) & 255u;
+            a.v[origin + tok * ld + 16 * i + c] = tok < have && tile ? value_of<BITS>(m, q) : 0.0f;
+        }
+    }
+}
+
+template <typename Args, typename Kernel>
+hipError_t launch(Kernel kernel, const Args &a, int parts, hipStream_t stream) {
+    const int64_t tiles = tiles_of(a.c.max_rows);
+    const int64_t waves = a.c.sequences * tiles * a.c.kv_heads * parts;
+    kernel<<<dim3(static_cast<uint32_t>((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a, static_cast<int>(tiles));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_append(int bits, int dim, const AppendArgs &a, hipStream_t stream) {
+    if (bits == 4)
+        return dim == 64    ? launch(append_kernel<4, 64>, a, 1, stream)
+               : dim == 128 ? launch(append_kernel<4, 128>, a, 2, stream)
+                            : launch(append_kernel<4, 256>, a, 4, stream);
+    return dim == 64    ? launch(append_kernel<8, 64>, a, 1, stream)
+           : dim == 128 ? launch(append_kernel<8, 128>, a, 2, stream)
+                        : launch(append_kernel<8, 256>, a, 4, stream);
+}
+
+hipError_t launch_cache_read(int bits, int dim, const ReadArgs &a, hipStream_t stream) {
+    if (bits == 4)
+        return dim == 64    ? launch(read_kernel<4, 64>, a, 1, stream)
+               : dim == 128 ? launch(read_kernel<4, 128>, a, 2, stream)
+                            : launch(read_kernel<4, 256>, a, 4, stream);
+    return dim == 64    ? launch(read_kernel<8, 64>, a, 1, stream)
+           : dim == 128 ? launch(read_kernel<8, 128>, a, 2, stream)
+                        : launch(read_kernel<8, 256>, a, 4, stream);
+}
+
+}  // namespace q8

@@ -73,7 +73,8 @@ def _on_stream(stream, device, fn, *args):
     with torch.cuda.stream(stream):
         result = fn(*args)
     for t in result if isinstance(result, tuple) else (result,):
-        t.record_stream(caller)  # where the caller, once it has waited, reads it
+        if t is not None:
+            t.record_stream(caller)  # where the caller, once it has waited, reads it
     return result
 
 
