@@ -1,0 +1,194 @@
+// attention.h -- what the attention's kernels share: the cache's values as operands of
+// the f16 matrix cores, queries and weights in two binary16 words, the end of a row.
+//
+// Every value of the cache is a binary16 number times a power of two exactly, so one side of
+// each product needs no rounding, and the f32 side is split in two words, x = hi + lo with
+// hi = rne16(x), lo = rne16(x - hi): 22 bits or more of it.  Both words go through the matrix
+// cores into the same f32 sums.
+//
+// v_mfma_f32_16x16x32_f16, as its lanes hold it (lane = 16 g + c):
+//   A: row c, depth 8 g + e (e = 0 .. 7);  B: column c, depth 8 g + e;  C: column c, rows 4 g + r
+// A product's depth may be taken in any order, if both operands take the same.
+//   scores: A = keys (row c of half i is token 8 (c / 4) + 4 i + c % 4 of the tile), B = queries
+//     (column c is row c of the workgroup's), depth = dimensions.  Lane (g, c) gets row c's scores
+//     of the tokens 8 g + 4 i + r, i = 0, 1.
+//   output: A = values (row c is a dimension), B = weights, depth = tokens: lane (g, c) gives the
+//     weights of tokens 8 g .. 8 g + 7 to row c, which are the ones it has just computed.
+// So scores turn into weights without leaving their lane.
+#pragma once
+
+#include "cache.h"
+#include "device.h"
+
+namespace q8 {
+
+using half2 = _Float16 __attribute__((ext_vector_type(2)));
+using half8 = _Float16 __attribute__((ext_vector_type(8)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNoMax = -3.0e38f;   // the maximum of no scores: weights of masked tokens are then 0, too
+constexpr float kWeightShift = 15.0f;  // weights are exp2(z - max + 15): far from binary16's smallest
+
+__device__ __forceinline__ half2 as_half2(uint32_t v) { return __builtin_bit_cast(half2, v); }
+__device__ __forceinline__ half2 splat(_Float16 v) { return half2{v, v}; }
+
+// How an operand's values follow from codes and a word: v = code' * d + c, exactly, where code' is
+// the code under the exponent of 16 (4 bits: 16 + n) or 1024 (8 bits: 1024 + n + 128).  d is the
+// scale times kDown: with the scale itself c would pass binary16's range (31 * 4352, 1152 * 512),
+// and the scales' lowest bits (2^-19, 2^-17) leave room below.  c = -(16 + z) d has 5 + 6 bits,
+// c = -1152 d 4 + 4, so that both are exact and the sum's exact value, a multiple of d, is, too.
+template <int BITS>
+struct Scales {
+    half2 d, c;
+
+    static constexpr float kDown = BITS == 4 ? 0.25f : 0.0625f;
+    static constexpr float kUp = 1.0f / kDown;
+
+    // of two words
+    __device__ __forceinline__ void set(uint32_t words) {
+        if (BITS == 4) {
+            d = as_half2(words & 0x7fe07fe0u) * splat(static_cast<_Float16>(kDown));
+            c = as_half2((words << 6 & 0x03c003c0u) | 0x4c004c00u) * -d;
+        } else {
+            d = as_half2(words) * splat(static_cast<_Float16>(kDown));
+            c = d * splat(static_cast<_Float16>(-1152.0f));
+        }
+    }
+};
+
+__device__ __forceinline__ half8 join(half2 a, half2 b, half2 c, half2 d) {
+    return half8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Eight codes: a dword of 4 bits, in pairs (0, 4), (1, 5), (2, 6), (3, 7); s[p] the scales of pair p.
+__device__ __forceinline__ half8 values_of(uint32_t x, const Scales<4> &s0, const Scales<4> &s1, const Scales<4> &s2,
+                                           const Scales<4> &s3) {
+    constexpr uint32_t m = 0x03c003c0u, e = 0x4c004c00u;
+    const half2 h0 = as_half2((x << 6 & m) | e), h1 = as_half2((x << 2 & m) | e), h2 = as_half2((x >> 2 & m) | e),
+                h3 = as_half2((x >> 6 & m) | e);
+    return join(__builtin_elementwise_fma(h0, s0.d, s0.c), __builtin_elementwise_fma(h1, s1.d, s1.c),
+                __builtin_elementwise_fma(h2, s2.d, s2.c), __builtin_elementwise_fma(h3, s3.d, s3.c));
+}
+
+// Eight codes: two dwords of 8 bits, in the bytes' order.
+__device__ __forceinline__ half8 values_of(uint32_t x, uint32_t y, const Scales<8> &s0, const Scales<8> &s1,
+                                           const Scales<8> &s2, const Scales<8> &s3) {
+    constexpr uint32_t e = 0x64646464u;
+    const half2 h0 = as_half2(__builtin_amdgcn_perm(e, x, 0x04010400u)), h1 = as_half2(__builtin_amdgcn_perm(e, x, 0x04030402u)),
+                h2 = as_half2(__builtin_amdgcn_perm(e, y, 0x04010400u)), h3 = as_half2(__builtin_amdgcn_perm(e, y, 0x04030402u));
+    return join(__builtin_elementwise_fma(h0, s0.d, s0.c), __builtin_elementwise_fma(h1, s1.d, s1.c),
+                __builtin_elementwise_fma(h2, s2.d, s2.c), __builtin_elementwise_fma(h3, s3.d, s3.c));
+}
+
+__device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Eight f32 as two binary16 words.
+__device__ __forceinline__ void two_words(const float (&x)[8], half8 &hi, half8 &lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const _Float16 h = static_cast<_Float16>(x[e]);
+        hi[e] = h;
+        lo[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h), -1.0f, x[e]));
+    }
+}
+
+// The largest, and the sum, over the four lanes l % 16 + 16 g.  (A swap of a register with its copy
+// leaves a lane's own value in one of them and its partner's in the other.)
+__device__ __forceinline__ float2 lane_pair32(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return make_float2(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float2 lane_pair16(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return make_float2(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float column_max(float v) {
+    const float2 a = lane_pair32(v), b = lane_pair16(fmaxf(a.x, a.y));
+    return fmaxf(b.x, b.y);
+}
+__device__ __forceinline__ float column_sum(float v) {
+    const float2 a = lane_pair32(v), b = lane_pair16(a.x + a.y);
+    return b.x + b.y;
+}
+
+__device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// The first dimension of the eight that step s of a score's product takes in lane group g; a lane's
+// codes lie together, up to 16 bytes.
+template <int BITS, int D>
+__device__ __forceinline__ constexpr int key_dims(int s, int g) {
+    if (BITS == 8) return 64 * (s / 2) + 16 * g + 8 * (s % 2);
+    return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s % 4);
+}
+
+// A power of two that brings values of up to `most` into [2^14, 2^15) (small ones below), as its f32
+// exponent field.
+__device__ __forceinline__ uint32_t lift_of(float most) {
+    const int e = static_cast<int>(__builtin_bit_cast(uint32_t, most) >> 23);  // biased
+    return static_cast<uint32_t>(min(141 + 127 - e, 253)) << 23;
+}
+
+// A query row as B operands of the scores' products: q * scale * log2(e), lifted, at step s's lane in
+// `hi` and `lo` (64 lanes of 16 bytes a step and word, hi before lo).  The row is lane column c's (null:
+// none, zeros).  Returns what a score is multiplied by: a power of two.
+template <int BITS, int D>
+__device__ __forceinline__ float load_query(const float *row, float scale, int lane, half8 *words) {
+    const int g = lane >> 4;
+    float x[D / 32][8];
+    float most = 0.0f;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (row) {
+            const float4 *p = reinterpret_cast<const float4 *>(row + key_dims<BITS, D>(s, g));
+            a = p[0], b = p[1];
+        }
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // the order of values_of: pairs (0, 4), (1, 5), .. of 4 bits
+            x[s][e] = v[BITS == 4 ? (e >> 1) + 4 * (e & 1) : e] * (scale * kLog2e);
+            most = fmaxf(most, fabsf(x[s][e]));
+        }
+    }
+    const uint32_t lift = lift_of(column_max(most));
+    const float f = __builtin_bit_cast(float, lift);
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] *= f;
+        half8 hi, lo;
+        two_words(x[s], hi, lo);
+        words[(2 * s) * 64 + lane] = hi;
+        words[(2 * s + 1) * 64 + lane] = lo;
+    }
+    return __builtin_bit_cast(float, (254u << 23) - lift) * Scales<BITS>::kUp;
+}
+
+// The dimensions of the output's products.  A lane's value codes come as kChunks 16-byte chunks of
+// the layout, kIn operands each.  Row c of operand (m, w) is dimension out_dim(c, m, w): with a
+// lane's chunks side by side, its dimensions lie in 2 (4 bits) or 1 blocks, and it needs the words of those alone.
+template <int BITS, int D>
+struct Out {
+    static constexpr int kChunks = BITS == 4 ? D / 64 : D / 32;
+    static constexpr int kIn = BITS == 4 ? 4 : 2;
+    static constexpr int kBlocks = BITS == 4 ? 2 : 1;
+    static constexpr int kPer = 16 / kChunks;  // rows of one unit of the layout
+    static constexpr int kUnit = BITS == 4 ? 64 : 32;  // dimensions of it
+
+    static __device__ __forceinline__ int unit(int c) { return c / kPer; }
+    static __device__ __forceinline__ int chunk(int c, int m) { return c % kPer * kChunks + m; }
+    static __device__ __forceinline__ int out_dim(int c, int m, int w) { return unit(c) * kUnit + 16 * w + chunk(c, m); }
+};
+
+}  // namespace q8

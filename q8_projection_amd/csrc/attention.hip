@@ -3,6 +3,8 @@
 // One wave a row and query head, one tile of 32 tokens at a time with the running
 // maximum and sum of the softmax: a lane's token for the scores, a lane's dimensions for
 // the values.
+#include <algorithm>
+
 #include "cache.h"
 #include "device.h"
 
@@ -82,9 +84,14 @@ hipError_t launch(const AttentionArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attention_workspace(int, const AttentionArgs &) { return 16; }
+int64_t attention_workspace(int dim, const AttentionArgs &a) {
+    AttentionArgs b = a;
+    b.c.max_rows = std::min(b.c.max_rows, std::max(kFewRows / b.group, 1));
+    return few_workspace(dim, b);
+}
 
-hipError_t launch_attention(int bits, int dim, const AttentionArgs &a, void *, hipStream_t stream) {
+hipError_t launch_attention(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream) {
+    if (int64_t(a.c.max_rows) * a.group <= kFewRows) return launch_few(bits, dim, a, workspace, stream);
     if (bits == 4)
         return dim == 64 ? launch<4, 64>(a, stream) : dim == 128 ? launch<4, 128>(a, stream) : launch<4, 256>(a, stream);
     return dim == 64 ? launch<8, 64>(a, stream) : dim == 128 ? launch<8, 128>(a, stream) : launch<8, 256>(a, stream);

@@ -118,6 +118,11 @@ __device__ __forceinline__ uint8_t *tile_at(const CacheArgs &c, int s, int t, in
 hipError_t launch_cache_append(int bits, int dim, const AppendArgs &a, hipStream_t stream);
 hipError_t launch_cache_read(int bits, int dim, const ReadArgs &a, hipStream_t stream);
 
+// Few rows a sequence and kv head: at most kFewRows.
+constexpr int kFewRows = 32;
+int64_t few_workspace(int dim, const AttentionArgs &a);
+hipError_t launch_few(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream);
+
 int64_t attention_workspace(int dim, const AttentionArgs &a);
 hipError_t launch_attention(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream);
 
