@@ -31,10 +31,21 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNoMax = -3.0e38f;   // the maximum of no scores: weights of masked tokens are then 0, too
-constexpr float kWeightShift = 15.0f;  // weights are exp2(z - max + 15): far from binary16's smallest
+// Weights are exp2(z - m + 11), with m at most 4 below the running maximum: sums are rescaled only where
+// the maximum has grown by more than 4, and a weight's words still end far below it (on binary16's
+// grid of 2^-24, 2^-36 of the largest weight) and never pass 2^15.
+constexpr float kWeightShift = 11.0f, kMaxSlack = 4.0f;
 
 __device__ __forceinline__ half2 as_half2(uint32_t v) { return __builtin_bit_cast(half2, v); }
 __device__ __forceinline__ half2 splat(_Float16 v) { return half2{v, v}; }
+
+// (x & mask) | bits as one instruction: the masks stay in a vector and a scalar register, where the
+// compiler would spend an instruction on each.
+__device__ __forceinline__ half2 and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(mask), "s"(bits));
+    return as_half2(r);
+}
 
 // How an operand's values follow from codes and a word: v = code' * d + c, exactly, where code' is
 // the code under the exponent of 16 (4 bits: 16 + n) or 1024 (8 bits: 1024 + n + 128).  d is the
@@ -52,7 +63,7 @@ struct Scales {
     __device__ __forceinline__ void set(uint32_t words) {
         if (BITS == 4) {
             d = as_half2(words & 0x7fe07fe0u) * splat(static_cast<_Float16>(kDown));
-            c = as_half2((words << 6 & 0x03c003c0u) | 0x4c004c00u) * -d;
+            c = and_or(words << 6, 0x03c003c0u, 0x4c004c00u) * -d;
         } else {
             d = as_half2(words) * splat(static_cast<_Float16>(kDown));
             c = d * splat(static_cast<_Float16>(-1152.0f));
@@ -68,8 +79,7 @@ __device__ __forceinline__ half8 join(half2 a, half2 b, half2 c, half2 d) {
 __device__ __forceinline__ half8 values_of(uint32_t x, const Scales<4> &s0, const Scales<4> &s1, const Scales<4> &s2,
                                            const Scales<4> &s3) {
     constexpr uint32_t m = 0x03c003c0u, e = 0x4c004c00u;
-    const half2 h0 = as_half2((x << 6 & m) | e), h1 = as_half2((x << 2 & m) | e), h2 = as_half2((x >> 2 & m) | e),
-                h3 = as_half2((x >> 6 & m) | e);
+    const half2 h0 = and_or(x << 6, m, e), h1 = and_or(x << 2, m, e), h2 = and_or(x >> 2, m, e), h3 = and_or(x >> 6, m, e);
     return join(__builtin_elementwise_fma(h0, s0.d, s0.c), __builtin_elementwise_fma(h1, s1.d, s1.c),
                 __builtin_elementwise_fma(h2, s2.d, s2.c), __builtin_elementwise_fma(h3, s3.d, s3.c));
 }
@@ -88,14 +98,21 @@ __device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Eight f32 as two binary16 words.
+// Eight f32 as two binary16 words.  (The empty asms make the pair one value, which else is converted half by
+// half once more for the difference, and hide the factor: a mixed multiply-add takes the words as they are.)
 __device__ __forceinline__ void two_words(const float (&x)[8], half8 &hi, half8 &lo) {
+    half2 h[4], l[4];
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const _Float16 h = static_cast<_Float16>(x[e]);
-        hi[e] = h;
-        lo[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h), -1.0f, x[e]));
+    for (int p = 0; p < 4; ++p) {
+        h[p] = half2{static_cast<_Float16>(x[2 * p]), static_cast<_Float16>(x[2 * p + 1])};
+        asm("" : "+v"(h[p]));
+        l[p] = half2{static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h[p].x), minus, x[2 * p])),
+                     static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h[p].y), minus, x[2 * p + 1]))};
     }
+    hi = join(h[0], h[1], h[2], h[3]);
+    lo = join(l[0], l[1], l[2], l[3]);
 }
 
 // The largest, and the sum, over the four lanes l % 16 + 16 g.  (A swap of a register with its copy
@@ -189,6 +206,27 @@ struct Out {
     static __device__ __forceinline__ int unit(int c) { return c / kPer; }
     static __device__ __forceinline__ int chunk(int c, int m) { return c % kPer * kChunks + m; }
     static __device__ __forceinline__ int out_dim(int c, int m, int w) { return unit(c) * kUnit + 16 * w + chunk(c, m); }
+
+    // fn(first dimension, four values) for lane group g's part of a row's sums.
+    template <typename Fn>
+    static __device__ __forceinline__ void for_each_vec(const f32x4 (&acc)[kChunks][kIn], int g, Fn fn) {
+#pragma unroll
+        for (int w = 0; w < kIn; ++w) {
+            if constexpr (kChunks == 1) {
+                fn(out_dim(4 * g, 0, w), acc[0][w]);
+            } else if constexpr (kChunks == 2) {
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                    fn(out_dim(4 * g + r, 0, w), f32x4{acc[0][w][r], acc[1][w][r], acc[0][w][r + 1], acc[1][w][r + 1]});
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int m = 0; m < kChunks; m += 4)
+                        fn(out_dim(4 * g + r, m, w), f32x4{acc[m][w][r], acc[m + 1][w][r], acc[m + 2][w][r], acc[m + 3][w][r]});
+            }
+        }
+    }
 };
 
 }  // namespace q8

@@ -15,17 +15,18 @@
 namespace q8 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kPiecesPerCu = 3;
-constexpr int kMinTiles = 16;  // tiles of a piece, at least (but for shorter sequences)
+constexpr int kAhead = 8;      // parts whose loads are in flight at once
+constexpr int kMinTiles = 16;  // tiles of a piece of four waves, at least (but for shorter sequences)
+constexpr int kPiecesPerSlot = 2;  // pieces for each workgroup that the chip holds
+constexpr int kBigItems = 4;       // kv heads for a CU, inverse, up to which a workgroup takes a whole CU
 
 struct FewArgs {
     AttentionArgs a;
     int pieces;         // wanted
+    int least;          // tiles of a piece, at least (but for shorter sequences)
     uint32_t *arrived;  // [2 pieces], zero between calls
     float *parts;       // [2 pieces][slot]
-    int slot;           // floats of a part: rows * (D + 2)
+    int slot;           // floats of a part: rows * (D + 4)
 };
 
 // Tiles that sequence s's rows see, [first, first + n).  A sequence without any keeps one, which
@@ -67,23 +68,25 @@ struct Keys {
     u32x4 x[2][kUnits];                                                  // (4 bits, D 64: half of it)
     uint32_t w[kUnits];
 
-    __device__ __forceinline__ void load(const uint8_t *tile, int g, int c) {
+    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t g, uint32_t c) {
         using T = Tile<BITS, D>;
-        const int t = (c >> 2) * 8 + (c & 3);  // token of half 0
+        // (unsigned offsets from a uniform pointer: no 64-bit arithmetic in the lanes)
+        const uint32_t t = (c >> 2) * 8 + (c & 3);  // token of half 0
+        const uint32_t code = t * T::kRow + g * (BITS == 4 && D == 64 ? 8 : 16);
+        const uint32_t word = T::kKeyWords + (c * T::kBlocks + (BITS == 4 && D > 64 ? g : g >> 1)) * 4;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint8_t *p = tile + (t + 4 * i) * T::kRow;
+                const uint8_t *p = tile + 4 * i * T::kRow + u * 64;
                 if (BITS == 4 && D == 64) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(p + g * 8);
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(p + code);
                     x[i][u] = u32x4{v.x, v.y, 0, 0};
                 } else {
-                    x[i][u] = *reinterpret_cast<const u32x4 *>(p + u * 64 + g * 16);
+                    x[i][u] = *reinterpret_cast<const u32x4 *>(p + code);
                 }
             }
-            const int block = BITS == 4 ? (D == 64 ? g >> 1 : 4 * u + g) : 2 * u + (g >> 1);
-            w[u] = *reinterpret_cast<const uint32_t *>(tile + T::kKeyWords + (c * T::kBlocks + block) * 4);
+            w[u] = *reinterpret_cast<const uint32_t *>(tile + u * (BITS == 4 ? 16 : 8) + word);
         }
     }
 };
@@ -93,15 +96,15 @@ struct Values {
     using O = Out<BITS, D>;
     u32x4 x[O::kChunks], w[O::kBlocks];
 
-    __device__ __forceinline__ void load(const uint8_t *tile, int g, int c) {
+    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t g, uint32_t c) {
         using T = Tile<BITS, D>;
-        const int u = O::unit(c);
+        const uint32_t u = O::unit(c);
+        const uint32_t code = T::kValues + ((u * 4 + g) * 16 + O::chunk(c, 0)) * 16;
+        const uint32_t word = T::kValueWords + (u * O::kBlocks * 4 + g) * 16;
 #pragma unroll
-        for (int m = 0; m < O::kChunks; ++m)
-            x[m] = *reinterpret_cast<const u32x4 *>(tile + T::kValues + ((u * 4 + g) * 16 + O::chunk(c, m)) * 16);
+        for (int m = 0; m < O::kChunks; ++m) x[m] = *reinterpret_cast<const u32x4 *>(tile + m * 16 + code);
 #pragma unroll
-        for (int b = 0; b < O::kBlocks; ++b)
-            w[b] = *reinterpret_cast<const u32x4 *>(tile + T::kValueWords + ((u * O::kBlocks + b) * 4 + g) * 16);
+        for (int b = 0; b < O::kBlocks; ++b) w[b] = *reinterpret_cast<const u32x4 *>(tile + b * 64 + word);
     }
 };
 
@@ -169,9 +172,9 @@ struct Wave {
             float most = z[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) most = fmaxf(most, z[e]);
-            most = column_max(most) * to_score[n];
-            if (__any(most > top[n])) {
-                const float now = fmaxf(most, top[n]);
+            most *= to_score[n];
+            if (__any(most > top[n] + kMaxSlack)) {
+                const float now = fmaxf(column_max(most), top[n]);
                 const float keep = exp2_of(top[n] - now);
                 top[n] = now;
                 sum[n] *= keep;
@@ -238,20 +241,40 @@ __device__ __forceinline__ void write_row(const AttentionArgs &a, const Where &a
         a.lse[at.row * a.heads + at.head] = total > 0 ? (top - kWeightShift) * kLn2 + logf(total) : -INFINITY;
 }
 
-__device__ __forceinline__ void store_agent(float *p, float x, float y) {
-    const uint64_t v = (uint64_t(__builtin_bit_cast(uint32_t, y)) << 32) | __builtin_bit_cast(uint32_t, x);
-    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Parts go to the workspace and come back past the XCDs' own caches (agent scope: sc1), 16 bytes at a
+// time, which the language's atomics do not offer.
+constexpr int kAgent = 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t parts_of(float *p, int floats) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, 0, floats * 4, 0x00020000);
 }
-__device__ __forceinline__ float2 load_agent(const float *p) {
-    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return make_float2(__builtin_bit_cast(float, static_cast<uint32_t>(v)), __builtin_bit_cast(float, static_cast<uint32_t>(v >> 32)));
+__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t r, int at, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at * 4, 0, kAgent);
 }
+__device__ __forceinline__ f32x4 load_part(__amdgpu_buffer_rsrc_t r, int at) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at * 4, 0, kAgent));
+}
+
+// A softmax's sums so far, and more of them.
+struct Sums {
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float top = kNoMax, sum = 0.0f;
+
+    __device__ __forceinline__ void add(f32x4 o2, float top2, float sum2) {
+        const float now = fmaxf(top, top2);
+        const float keep = exp2_of(top - now), more = exp2_of(top2 - now);
+        top = now;
+        sum = sum * keep + sum2 * more;
+        o = o * keep + o2 * more;
+    }
+};
 
 // A piece: tiles [from, to) of the span of a sequence, for one kv head; piece `index` of `n` of it, whose
 // parts are first, first + 1, ..
 struct Piece {
     int s, head, index, n;
     int64_t first;
+    Rows rows;
+    Span span;
 };
 
 // Finds piece after piece, in ascending order.
@@ -259,15 +282,19 @@ struct Pieces {
     int target;               // tiles of a piece at most
     int s0 = 0;               // sequences s0 .. s0 + 63 are the lanes'
     int64_t pieces = 0, parts = 0;  // before them
+    Rows rows;
+    Span span;
     uint32_t count, scan, scan_parts;
 
-    __device__ __forceinline__ void look(const AttentionArgs &a, int lane) {
+    __device__ __forceinline__ uint32_t look(const AttentionArgs &a, int lane) {
         const int s = s0 + lane;
-        const int n = s < a.c.sequences ? span_of(a, sequence_rows(a.c, s)).n : 0;
-        set(n);
+        rows = Rows{0, 0, 0, 0};
+        if (s < a.c.sequences) rows = sequence_rows(a.c, s);
+        span = span_of(a, rows);
+        return static_cast<uint32_t>(span.n);
     }
-    __device__ __forceinline__ void set(int n) {
-        count = static_cast<uint32_t>((n + target - 1) / target);
+    __device__ __forceinline__ void divide() {
+        count = static_cast<uint32_t>((span.n + target - 1) / target);
         scan = wave_scan(count);
         scan_parts = wave_scan(count > 1 ? count : 0u);
     }
@@ -280,6 +307,9 @@ struct Pieces {
                 const int64_t before = pieces + (l ? int64_t(lane_of(scan, l - 1)) * a.c.kv_heads : 0);
                 out.s = s0 + l;
                 out.n = static_cast<int>(lane_of(count, l));
+                out.rows = Rows{static_cast<int>(lane_of(rows.first, l)), static_cast<int>(lane_of(rows.n, l)),
+                                static_cast<int>(lane_of(rows.at, l)), static_cast<int>(lane_of(rows.end, l))};
+                out.span = Span{static_cast<int>(lane_of(span.first, l)), static_cast<int>(lane_of(span.n, l))};
                 const int rest = static_cast<int>(p - before);
                 out.head = rest / out.n;
                 out.index = rest - out.head * out.n;
@@ -291,19 +321,26 @@ struct Pieces {
             parts += int64_t(lane_of(scan_parts, 63)) * a.c.kv_heads;
             s0 += 64;
             look(a, lane);
+            divide();
         }
     }
 };
 
+// Waves of a SIMD that the registers allow without a spill (a kernel with scratch memory starts 5 us
+// later).
 template <int BITS, int D, int NR>
-__global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_kernel(FewArgs f) {
+constexpr int kWavesPerSimd = NR == 1 && (D == 64 || (D == 128 && BITS == 4)) ? 3 : 2;
+
+template <int BITS, int D, int NR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_kernel(FewArgs f) {
     using O = Out<BITS, D>;
+    constexpr int kThreads = 64 * WAVES;
     constexpr int kRows = 16 * NR;
     constexpr int kPad = D + 4;
-    constexpr int kQuery = NR * (D / 32) * 2 * 64 * 16;       // bytes of the queries' words
-    constexpr int kMeet = kWaves / 2 * kRows * kPad * 4;      // of the waves' sums
+    constexpr int kQuery = NR * (D / 32) * 2 * 64 * 16;  // bytes of the queries' words
+    constexpr int kMeet = WAVES * 16 * kPad * 4;         // of the waves' sums, 16 rows at a time
     __shared__ __align__(16) uint8_t shared[kQuery > kMeet ? kQuery : kMeet];
-    __shared__ float tops[kWaves][kRows], sums[kWaves][kRows], to_scores[kRows];
+    __shared__ float tops[WAVES][kRows], sums[WAVES][kRows], to_scores[kRows];
     __shared__ uint32_t last;
     half8 *query = reinterpret_cast<half8 *>(shared);
     float *meet = reinterpret_cast<float *>(shared);
@@ -313,23 +350,19 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     // How many tiles there are, and so how many make a piece.
-    int64_t total = 0;
-    int tiles = 0;
-    for (int s0 = 0; s0 < c.sequences; s0 += 64) {
-        const int s = s0 + lane;
-        tiles = s < c.sequences ? span_of(a, sequence_rows(c, s)).n : 0;
-        total += lane_of(wave_scan(tiles), 63);
-    }
     Pieces pieces;
+    int64_t total = 0;
+    for (; pieces.s0 < c.sequences; pieces.s0 += 64) total += lane_of(wave_scan(pieces.look(a, lane)), 63);
     // (no sequence has more than 2^25 tiles)
-    pieces.target = static_cast<int>(min(max((total * c.kv_heads + f.pieces - 1) / f.pieces, int64_t(kMinTiles)), int64_t(1) << 26));
-    if (c.sequences <= 64) pieces.set(tiles);
-    else pieces.look(a, lane);
+    pieces.target = static_cast<int>(min(max((total * c.kv_heads + f.pieces - 1) / f.pieces, int64_t(f.least)), int64_t(1) << 26));
+    pieces.s0 = 0;
+    if (c.sequences > 64) pieces.look(a, lane);
+    pieces.divide();
 
     Piece piece;
     for (int64_t p = blockIdx.x; pieces.find(a, p, lane, piece); p += gridDim.x) {
-        const Rows r = sequence_rows(c, piece.s);
-        const Span span = span_of(a, r);
+        const Rows r = piece.rows;
+        const Span span = piece.span;
         const int from = static_cast<int>(int64_t(span.n) * piece.index / piece.n);
         const int to = static_cast<int>(int64_t(span.n) * (piece.index + 1) / piece.n);
         const int rows = r.n * a.group, head = piece.head;
@@ -341,14 +374,14 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
         const int shift = c.page_shift - 5;
         int base = from + wid, mine = 0, page = -1;
         const auto look_up = [&] {
-            mine = base < to ? min((to - base + kWaves - 1) / kWaves, 64) : 0;
-            const int t = span.first + base + lane * kWaves;
+            mine = base < to ? min((to - base + WAVES - 1) / WAVES, 64) : 0;
+            const int t = span.first + base + lane * WAVES;
             page = -1;
             if (lane < mine && t * kTileTokens < hi) page = c.table[piece.s * c.table_ld + (t >> shift)];
             if (page < 0 || page >= c.pages) page = -1;
         };
         const auto tile_of = [&](int l) -> const uint8_t * {
-            const int t = span.first + base + l * kWaves;
+            const int t = span.first + base + l * WAVES;
             const int64_t pg = max(__builtin_amdgcn_readlane(page, l), 0);  // (none: the pool's first, not looked at)
             return c.data + (((pg * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes;
         };
@@ -393,7 +426,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
 
         while (mine) {
             for (int l = 0; l < mine; ++l) {
-                const int t0 = (span.first + base + l * kWaves) * kTileTokens;
+                const int t0 = (span.first + base + l * WAVES) * kTileTokens;
                 const Seen seen = {t0 < all_lo || t0 + kTileTokens > all_hi, t0, lo, hi};
                 const bool there = __builtin_amdgcn_readlane(page, l) >= 0;
                 const uint8_t *next = tile_of(min(l + 1, mine - 1));
@@ -406,7 +439,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
                 }
                 values.load(next, g, col);
             }
-            base += 64 * kWaves;
+            base += 64 * WAVES;
             look_up();
             if (mine) {
                 const uint8_t *tile = tile_of(0);
@@ -415,82 +448,42 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
             }
         }
 
-        // The waves' sums meet: half of the waves give theirs to the other half, until one has all.
+        // The waves' sums meet, 16 rows at a time: all write theirs, every thread adds up some.
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float all = column_sum(w.sum[n]);
             if (g == 0) tops[wid][n * 16 + col] = w.top[n], sums[wid][n * 16 + col] = all;
         }
         __syncthreads();  // and the queries' words are free
-        float top[NR], sum[NR];
+        // parts of a kv head: rows of D sums each, then rows of (maximum, sum)
+        const int vecs = rows * (D / 4);  // 16-byte pieces of the rows
+        const __amdgpu_buffer_rsrc_t parts = parts_of(f.parts + piece.first * f.slot, piece.n * f.slot);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const int x = n * 16 + col;
-            top[n] = tops[0][x];
+            if (n) __syncthreads();
+            float top = tops[0][n * 16 + col];
 #pragma unroll
-            for (int v = 1; v < kWaves; ++v) top[n] = fmaxf(top[n], tops[v][x]);
-            sum[n] = 0.0f;
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) sum[n] += sums[v][x] * exp2_of(tops[v][x] - top[n]);
-            const float f = exp2_of(w.top[n] - top[n]) * Scales<BITS>::kUp;
-#pragma unroll
-            for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-                for (int j = 0; j < O::kIn; ++j) w.acc[n][m][j] *= f;
-        }
-#pragma unroll
-        for (int half = kWaves / 2; half >= 1; half /= 2) {
-            if (wid >= half && wid < 2 * half) {
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-                    if (n * 16 + col < rows)
-#pragma unroll
-                        for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-                            for (int j = 0; j < O::kIn; ++j)
-                                *reinterpret_cast<f32x4 *>(meet + ((wid - half) * kRows + n * 16 + col) * kPad + ((m * O::kIn + j) * 4 + g) * 4) = w.acc[n][m][j];
-            }
+            for (int v = 1; v < WAVES; ++v) top = fmaxf(top, tops[v][n * 16 + col]);
+            const float scale = exp2_of(w.top[n] - top) * Scales<BITS>::kUp;
+            if (n * 16 + col < rows) O::for_each_vec(w.acc[n], g, [&](int dim, f32x4 v) {
+                *reinterpret_cast<f32x4 *>(meet + (wid * 16 + col) * kPad + dim) = v * scale;
+            });
             __syncthreads();
-            if (wid < half) {
+            for (int e = threadIdx.x; e < min(vecs - n * 4 * D, 4 * D); e += kThreads) {
+                const int y = e / (D / 4), x = n * 16 + y, dim = e % (D / 4) * 4;
+                f32x4 o = *reinterpret_cast<const f32x4 *>(meet + y * kPad + dim);
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
-                    if (n * 16 + col < rows)
+                for (int v = 1; v < WAVES; ++v) o += *reinterpret_cast<const f32x4 *>(meet + (v * 16 + y) * kPad + dim);
+                if (piece.n > 1) store_part(parts, piece.index * f.slot + x * D + dim, o);
+                if (piece.n == 1 || dim == 0) {
+                    float top_x = tops[0][x], sum_x = 0.0f;
 #pragma unroll
-                        for (int m = 0; m < O::kChunks; ++m)
+                    for (int v = 1; v < WAVES; ++v) top_x = fmaxf(top_x, tops[v][x]);
 #pragma unroll
-                            for (int j = 0; j < O::kIn; ++j)
-                                w.acc[n][m][j] += *reinterpret_cast<const f32x4 *>(meet + (wid * kRows + n * 16 + col) * kPad + ((m * O::kIn + j) * 4 + g) * 4);
-            }
-            __syncthreads();
-        }
-        // wave 0 has the piece's sums; they go out by whole rows
-        if (wid == 0) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-                if (n * 16 + col < rows)
-#pragma unroll
-                    for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-                        for (int j = 0; j < O::kIn; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                meet[(n * 16 + col) * kPad + O::out_dim(4 * g + e, m, j)] = w.acc[n][m][j][e];
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-                if (g == 0) tops[0][n * 16 + col] = top[n], sums[0][n * 16 + col] = sum[n];
-        }
-        __syncthreads();
-        float *part = f.parts + (piece.first + piece.index) * f.slot;
-        for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
-            const int x = e / (D / 4), dim = e % (D / 4) * 4;
-            const f32x4 o = *reinterpret_cast<const f32x4 *>(meet + x * kPad + dim);
-            if (piece.n == 1) {
-                write_row<D>(a, where(a, r, head, x), dim, o, sums[0][x], tops[0][x]);
-            } else {
-                float *dst = part + x * D + dim;
-                store_agent(dst, o.x, o.y);
-                store_agent(dst + 2, o.z, o.w);
-                if (dim == 0) store_agent(part + rows * D + 2 * x, tops[0][x], sums[0][x]);
+                    for (int v = 0; v < WAVES; ++v) sum_x += sums[v][x] * exp2_of(tops[v][x] - top_x);
+                    if (piece.n == 1) write_row<D>(a, where(a, r, head, x), dim, o, sum_x, top_x);
+                    else store_part(parts, piece.index * f.slot + (vecs + x) * 4, f32x4{top_x, sum_x, 0.f, 0.f});
+                }
             }
         }
         if (piece.n > 1) {
@@ -504,32 +497,44 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
             }
             __syncthreads();
             if (last) {
-                const float *first = f.parts + piece.first * f.slot;
-                for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+                // Few rows leave threads over: these divide the parts, slice after slice of them.
+                const int slices = vecs < kThreads ? kThreads / vecs : 1;
+                const int slice = vecs < kThreads ? threadIdx.x / vecs : 0;
+                const int i0 = piece.n * slice / slices, i1 = piece.n * (slice + 1) / slices;
+                f32x4 *there = reinterpret_cast<f32x4 *>(shared);
+                for (int e0 = 0; e0 < vecs; e0 += kThreads) {
+                    const int e = vecs < kThreads ? threadIdx.x - slice * vecs : e0 + threadIdx.x;
+                    const bool live = slice < slices && e < vecs;
                     const int x = e / (D / 4), dim = e % (D / 4) * 4;
-                    float top_x = kNoMax, sum_x = 0.0f;
-                    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-                    constexpr int kAhead = 8;
-                    for (int i0 = 0; i0 < piece.n; i0 += kAhead) {
-                        float2 st[kAhead], v0[kAhead], v1[kAhead];
+                    Sums all;
+                    if (live) {
+                        for (int i = i0; i < i1; i += kAhead) {
+                            f32x4 o[kAhead], st[kAhead];
 #pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            const float *q = first + int64_t(min(i0 + i, piece.n - 1)) * f.slot;
-                            st[i] = load_agent(q + rows * D + 2 * x);
-                            v0[i] = load_agent(q + x * D + dim);
-                            v1[i] = load_agent(q + x * D + dim + 2);
-                        }
+                            for (int j = 0; j < kAhead; ++j) {
+                                // (past the last one: past the buffer, nothing is read)
+                                const int at_part = (i + j) * f.slot | static_cast<int>(oob_bit(i + j < i1) >> 2);
+                                st[j] = load_part(parts, at_part + (vecs + x) * 4);
+                                o[j] = load_part(parts, at_part + 4 * e);
+                            }
 #pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            if (i0 + i >= piece.n) break;
-                            const float now = fmaxf(top_x, st[i].x);
-                            const float keep = exp2_of(top_x - now), add = exp2_of(st[i].x - now);
-                            top_x = now;
-                            sum_x = sum_x * keep + st[i].y * add;
-                            o = o * keep + f32x4{v0[i].x, v0[i].y, v1[i].x, v1[i].y} * add;
+                            for (int j = 0; j < kAhead; ++j)
+                                if (i + j < i1) all.add(o[j], st[j].x, st[j].y);
                         }
                     }
-                    write_row<D>(a, where(a, r, head, x), dim, o, sum_x, top_x);
+                    if (slices > 1) {
+                        if (live && slice) {
+                            there[2 * (threadIdx.x - vecs)] = all.o;
+                            there[2 * (threadIdx.x - vecs) + 1] = f32x4{all.top, all.sum, 0.f, 0.f};
+                        }
+                        __syncthreads();
+                        if (live && !slice)
+                            for (int v = 1; v < slices; ++v) {
+                                const f32x4 st = there[2 * (threadIdx.x + (v - 1) * vecs) + 1];
+                                all.add(there[2 * (threadIdx.x + (v - 1) * vecs)], st.x, st.y);
+                            }
+                    }
+                    if (live && !slice) write_row<D>(a, where(a, r, head, x), dim, all.o, all.sum, all.top);
                 }
             }
         }
@@ -537,36 +542,51 @@ __global__ __launch_bounds__(kThreads, NR == 1 && D <= 128 ? 3 : 2) void few_ker
     }
 }
 
-int few_pieces() { return device_info().cus * kPiecesPerCu; }
-
-template <int BITS, int D>
-hipError_t run(const FewArgs &f, hipStream_t stream) {
-    // every piece a workgroup, unless there are very many
-    const int64_t most = f.pieces + int64_t(f.a.c.sequences) * f.a.c.kv_heads;
-    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(most, 32 * int64_t(f.pieces))));
-    if (f.a.c.max_rows * f.a.group <= 16) few_kernel<BITS, D, 1><<<grid, kThreads, 0, stream>>>(f);
-    else few_kernel<BITS, D, 2><<<grid, kThreads, 0, stream>>>(f);
+// Workgroups of 4 waves, as many as a CU holds, overlap one's start and end with another's tiles.  Where
+// a kv head is divided over many workgroups anyway, one of all the waves that a CU holds has a third
+// or half of the parts to join.
+template <int BITS, int D, int NR>
+hipError_t run(FewArgs f, hipStream_t stream) {
+    constexpr int kPerCu = kWavesPerSimd<BITS, D, NR>;
+    const int64_t items = int64_t(f.a.c.sequences) * f.a.c.kv_heads;
+    const int cus = device_info().cus;
+    if (items * kBigItems <= cus) {
+        f.pieces = cus;
+        f.least = kMinTiles * kPerCu;
+        few_kernel<BITS, D, NR, 4 * kPerCu><<<dim3(static_cast<uint32_t>(cus + items)), 256 * kPerCu, 0, stream>>>(f);
+    } else {
+        f.pieces = cus * kPiecesPerSlot * kPerCu;
+        f.least = kMinTiles;
+        // every piece a workgroup, unless there are very many
+        const int64_t most = std::min<int64_t>(f.pieces + items, 32 * int64_t(f.pieces));
+        few_kernel<BITS, D, NR, 4><<<dim3(static_cast<uint32_t>(most)), 256, 0, stream>>>(f);
+    }
     return hipGetLastError();
 }
 
-int64_t counter_bytes(int64_t pieces) { return (2 * pieces * 4 + 255) / 256 * 256; }
+template <int BITS, int D>
+hipError_t run_rows(const FewArgs &f, hipStream_t stream) {
+    return f.a.c.max_rows * f.a.group <= 16 ? run<BITS, D, 1>(f, stream) : run<BITS, D, 2>(f, stream);
+}
+
+int64_t most_pieces() { return int64_t(device_info().cus) * 3 * kPiecesPerSlot; }
+int64_t counter_bytes() { return (2 * most_pieces() * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
 int64_t few_workspace(int dim, const AttentionArgs &a) {
-    const int64_t pieces = few_pieces(), rows = int64_t(a.c.max_rows) * a.group;
-    return counter_bytes(pieces) + 2 * pieces * rows * (dim + 2) * 4;
+    return counter_bytes() + 2 * most_pieces() * a.c.max_rows * a.group * (dim + 4) * 4;
 }
 
 hipError_t launch_few(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream) {
     FewArgs f = {};
     f.a = a;
-    f.pieces = few_pieces();
     f.arrived = static_cast<uint32_t *>(workspace);
-    f.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + counter_bytes(f.pieces));
-    f.slot = a.c.max_rows * a.group * (dim + 2);
-    if (bits == 4) return dim == 64 ? run<4, 64>(f, stream) : dim == 128 ? run<4, 128>(f, stream) : run<4, 256>(f, stream);
-    return dim == 64 ? run<8, 64>(f, stream) : dim == 128 ? run<8, 128>(f, stream) : run<8, 256>(f, stream);
+    f.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + counter_bytes());
+    f.slot = a.c.max_rows * a.group * (dim + 4);
+    if (bits == 4)
+        return dim == 64 ? run_rows<4, 64>(f, stream) : dim == 128 ? run_rows<4, 128>(f, stream) : run_rows<4, 256>(f, stream);
+    return dim == 64 ? run_rows<8, 64>(f, stream) : dim == 128 ? run_rows<8, 128>(f, stream) : run_rows<8, 256>(f, stream);
 }
 
 }  // namespace q8

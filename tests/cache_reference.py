@@ -8,10 +8,10 @@ tokens that a row sees, and A = sum_t p_t |v_t| of its outputs:
       with the rounding of scale and q: under 2^-21; D products added in f32: at most D + 8
       roundings; the scale's, the difference's and the exponential's roundings
   a weight p_t is then off by 2 ez + 2^-21 (two words), relative, ez for the sum's as well
-  a weight is also off by 2^-40 of the largest one, absolute: its words are binary16 numbers of
-      up to 2^15 on a grid of 2^-24 (and f32 exponentials vanish under 2^-149)
+  a weight is also off by 2^-36 of the largest one, absolute: its words lie on binary16's grid of
+      2^-24 (half a step: 2^-25) where the largest is 2^11 or more (and f32 exponentials vanish under 2^-149)
   sums over the tokens are added in f32 in chains: at most (T / 8 + 64) 2^-24, relative to A
-so |out - ref| <= A (2 ez + 2^-20 + (T / 8 + 64) 2^-24) + 2^-40 sum_t |v_t| / sum_t exp(z_t - max z), and lse
+so |out - ref| <= A (2 ez + 2^-20 + (T / 8 + 64) 2^-24) + 2^-36 sum_t |v_t| / sum_t exp(z_t - max z), and lse
 is off by
 ez + (T / 8 + 64) 2^-24 + 2^-23 |lse| at most.
 
@@ -132,7 +132,7 @@ def attend(q, k, v, at, scale, window=0, have=None):
             ez = most * (2.0 ** -21 + (d + 8) * 2.0 ** -24) + 8 * 2.0 ** -24 * (1 + np.abs(z).max())
             chain = (len(z) / 8 + 64) * 2.0 ** -24
             size = (e / e.sum()) @ np.abs(vh)
-            out_bound[r, h] = size * (2 * ez + 2.0 ** -20 + chain) + 2.0 ** -40 * np.abs(vh).sum(0) / e.sum()
+            out_bound[r, h] = size * (2 * ez + 2.0 ** -20 + chain) + 2.0 ** -36 * np.abs(vh).sum(0) / e.sum()
             usual[r, h] = size * (2.0 ** -23 * (np.sqrt(d + 8) * most + 4 * (1 + np.abs(z).max())) + 2.0 ** -20 +
                                   np.sqrt(len(z)) * 2.0 ** -24)
             lse_bound[r, h] = ez + chain + 2.0 ** -23 * abs(lse[r, h])
