@@ -155,12 +155,11 @@ __device__ __forceinline__ uint32_t lift_of(float most) {
     return static_cast<uint32_t>(min(141 + 127 - e, 253)) << 23;
 }
 
-// A query row as B operands of the scores' products: q * scale * log2(e), lifted, at step s's lane in
-// `hi` and `lo` (64 lanes of 16 bytes a step and word, hi before lo).  The row is lane column c's (null:
-// none, zeros).  Returns what a score is multiplied by: a power of two.
-template <int BITS, int D>
-__device__ __forceinline__ float load_query(const float *row, float scale, int lane, half8 *words) {
-    const int g = lane >> 4;
+// A query row as B operands of the scores' products: q * scale * log2(e), lifted, out(step, hi, lo) for
+// each step.  The row is lane column c's (null: none, zeros).  Returns what a score is multiplied by:
+// a power of two.
+template <int BITS, int D, typename Fn>
+__device__ __forceinline__ float load_query(const float *row, float scale, int g, Fn out) {
     float x[D / 32][8];
     float most = 0.0f;
 #pragma unroll
@@ -186,8 +185,7 @@ __device__ __forceinline__ float load_query(const float *row, float scale, int l
         for (int e = 0; e < 8; ++e) x[s][e] *= f;
         half8 hi, lo;
         two_words(x[s], hi, lo);
-        words[(2 * s) * 64 + lane] = hi;
-        words[(2 * s + 1) * 64 + lane] = lo;
+        out(s, hi, lo);
     }
     return __builtin_bit_cast(float, (254u << 23) - lift) * Scales<BITS>::kUp;
 }
@@ -226,6 +224,122 @@ struct Out {
                         fn(out_dim(4 * g + r, m, w), f32x4{acc[m][w][r], acc[m + 1][w][r], acc[m + 2][w][r], acc[m + 3][w][r]});
             }
         }
+    }
+};
+
+// Tiles that sequence s's rows see, [first, first + n).  A sequence without any keeps one, which
+// has no token, so that its rows are written; one without rows has none.
+struct Span {
+    int first, n;
+};
+
+__device__ __forceinline__ Span span_of(const AttentionArgs &a, const Rows &r) {
+    if (r.n == 0) return {0, 0};
+    const int begin = a.window ? max(r.at - a.window + 1, 0) : 0;
+    const int end = min(r.at + r.n, r.end);
+    const int first = begin / kTileTokens;
+    return {first, max((end + kTileTokens - 1) / kTileTokens - first, 1)};
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t add_dpp(uint32_t v) {
+    return v + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v = add_dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+    v = add_dpp<0x112, 0xf>(v);
+    v = add_dpp<0x114, 0xf>(v);
+    v = add_dpp<0x118, 0xf>(v);
+    v = add_dpp<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+    return add_dpp<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
+}
+
+// Scores of 32 tokens (lane (g, c): row c, tokens 8 g + 4 i + r in s[i][r]) to weights in two words, with the
+// running maximum and sum of the softmax and the sums so far.  masked: only tokens t, t0 the first, of
+// [begin, end) are seen by the lane's row.
+template <int M, int N>
+__device__ __forceinline__ void weigh(const f32x4 (&s)[2], bool masked, int t0, int g, int begin, int end, float to_score,
+                                      float &top, float &sum, f32x4 (&acc)[M][N], half8 &hi, half8 &lo) {
+    float z[8];  // pairs (token p, token p + 4) of the lane's eight
+#pragma unroll
+    for (int p = 0; p < 4; ++p) z[2 * p] = s[0][p], z[2 * p + 1] = s[1][p];
+    if (masked) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = t0 + 8 * g + (e >> 1) + 4 * (e & 1);
+            z[e] = t >= begin && t < end ? z[e] : -INFINITY;
+        }
+    }
+    float most = z[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) most = fmaxf(most, z[e]);
+    most *= to_score;
+    if (__any(most > top + kMaxSlack)) {
+        const float now = fmaxf(column_max(most), top);
+        const float keep = exp2_of(top - now);
+        top = now;
+        sum *= keep;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int w = 0; w < N; ++w) acc[m][w] *= keep;
+    }
+    const float below = kWeightShift - top;
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        w[e] = exp2_of(__builtin_fmaf(z[e], to_score, below));
+        sum += w[e];
+    }
+    two_words(w, hi, lo);
+}
+
+// Row x of a sequence and kv head: which of the call's.
+struct Where {
+    int64_t row;
+    int head;
+};
+__device__ __forceinline__ Where where(const AttentionArgs &a, const Rows &r, int kv_head, int x) {
+    const int i = x / a.group;
+    return {int64_t(r.first) + i, kv_head * a.group + x - i * a.group};
+}
+
+template <int D>
+__device__ __forceinline__ void write_row(const AttentionArgs &a, const Where &at, int dim, f32x4 o, float total, float top) {
+    const float f = total > 0 ? 1.0f / total : 0.0f;
+    *reinterpret_cast<f32x4 *>(a.out + (at.row * a.heads + at.head) * D + dim) = o * f;
+    if (dim == 0 && a.lse)
+        a.lse[at.row * a.heads + at.head] = total > 0 ? (top - kWeightShift) * kLn2 + logf(total) : -INFINITY;
+}
+
+// Parts go to the workspace and come back past the XCDs' own caches (agent scope: sc1), 16 bytes at a
+// time, which the language's atomics do not offer.
+constexpr int kAgent = 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t parts_of(float *p, int floats) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, 0, floats * 4, 0x00020000);
+}
+__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at * 4, 0, kAgent);
+}
+__device__ __forceinline__ f32x4 load_part(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at * 4, 0, kAgent));
+}
+
+// A softmax's sums so far, and more of them.
+struct Sums {
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float top = kNoMax, sum = 0.0f;
+
+    __device__ __forceinline__ void add(f32x4 o2, float top2, float sum2) {
+        const float now = fmaxf(top, top2);
+        const float keep = exp2_of(top - now), more = exp2_of(top2 - now);
+        top = now;
+        sum = sum * keep + sum2 * more;
+        o = o * keep + o2 * more;
     }
 };
 

@@ -17,7 +17,8 @@ namespace {
 
 constexpr int kAhead = 8;      // parts whose loads are in flight at once
 constexpr int kMinTiles = 16;  // tiles of a piece of four waves, at least (but for shorter sequences)
-constexpr int kPiecesPerSlot = 2;  // pieces for each workgroup that the chip holds
+constexpr int kPiecesPerSlot = 2;  // pieces for each workgroup that the chip holds (twice as many counters: kCountersPerCu)
+static_assert(2 * 3 * kPiecesPerSlot <= kCountersPerCu);
 constexpr int kBigItems = 4;       // kv heads for a CU, inverse, up to which a workgroup takes a whole CU
 
 struct FewArgs {
@@ -28,37 +29,6 @@ struct FewArgs {
     float *parts;       // [2 pieces][slot]
     int slot;           // floats of a part: rows * (D + 4)
 };
-
-// Tiles that sequence s's rows see, [first, first + n).  A sequence without any keeps one, which
-// has no token, so that its rows are written; one without rows has none.
-struct Span {
-    int first, n;
-};
-
-__device__ __forceinline__ Span span_of(const AttentionArgs &a, const Rows &r) {
-    if (r.n == 0) return {0, 0};
-    const int begin = a.window ? max(r.at - a.window + 1, 0) : 0;
-    const int end = min(r.at + r.n, r.end);
-    const int first = begin / kTileTokens;
-    return {first, max((end + kTileTokens - 1) / kTileTokens - first, 1)};
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t add_dpp(uint32_t v) {
-    return v + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
-}
-// Inclusive sum over the lanes.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-    v = add_dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
-    v = add_dpp<0x112, 0xf>(v);
-    v = add_dpp<0x114, 0xf>(v);
-    v = add_dpp<0x118, 0xf>(v);
-    v = add_dpp<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
-    return add_dpp<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
-}
-__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
-}
 
 // Codes and words of a lane's keys, and of its values.
 template <int BITS, int D>
@@ -108,8 +78,7 @@ struct Values {
     }
 };
 
-// Which tokens of a tile count: [lo, hi) are there (others' codes may be anything), and row n of the
-// lane sees [begin, end).
+// Which tokens of a tile count: [lo, hi) are there, others' codes may be anything.
 struct Seen {
     bool masked;  // some token of the tile is not seen by some row, or is none
     int t0, lo, hi;
@@ -155,45 +124,6 @@ struct Wave {
         }
     }
 
-    // Scores to weights, with the running maximum and sum.
-    __device__ __forceinline__ void weights(f32x4 (&s)[NR][2], const Seen &seen, int g) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float z[8];  // pairs (token p, token p + 4) of the lane's eight
-#pragma unroll
-            for (int p = 0; p < 4; ++p) z[2 * p] = s[n][0][p], z[2 * p + 1] = s[n][1][p];
-            if (seen.masked) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = seen.t0 + 8 * g + (e >> 1) + 4 * (e & 1);
-                    z[e] = t >= max(begin[n], seen.lo) && t < min(end[n], seen.hi) ? z[e] : -INFINITY;
-                }
-            }
-            float most = z[0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) most = fmaxf(most, z[e]);
-            most *= to_score[n];
-            if (__any(most > top[n] + kMaxSlack)) {
-                const float now = fmaxf(column_max(most), top[n]);
-                const float keep = exp2_of(top[n] - now);
-                top[n] = now;
-                sum[n] *= keep;
-#pragma unroll
-                for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-                    for (int w = 0; w < O::kIn; ++w) acc[n][m][w] *= keep;
-            }
-            const float below = kWeightShift - top[n];
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                w[e] = exp2_of(__builtin_fmaf(z[e], to_score[n], below));
-                sum[n] += w[e];
-            }
-            two_words(w, p_hi[n], p_lo[n]);
-        }
-    }
-
     __device__ __forceinline__ void add_values(const Values<BITS, D> &v, const Seen &seen, int g) {
         Scales<BITS> sc[O::kBlocks][4];
 #pragma unroll
@@ -220,51 +150,6 @@ struct Wave {
                 }
             }
         }
-    }
-};
-
-// Row x of a sequence and kv head: which of the call's.
-struct Where {
-    int64_t row;
-    int head;
-};
-__device__ __forceinline__ Where where(const AttentionArgs &a, const Rows &r, int kv_head, int x) {
-    const int i = x / a.group;
-    return {int64_t(r.first) + i, kv_head * a.group + x - i * a.group};
-}
-
-template <int D>
-__device__ __forceinline__ void write_row(const AttentionArgs &a, const Where &at, int dim, f32x4 o, float total, float top) {
-    const float f = total > 0 ? 1.0f / total : 0.0f;
-    *reinterpret_cast<f32x4 *>(a.out + (at.row * a.heads + at.head) * D + dim) = o * f;
-    if (dim == 0 && a.lse)
-        a.lse[at.row * a.heads + at.head] = total > 0 ? (top - kWeightShift) * kLn2 + logf(total) : -INFINITY;
-}
-
-// Parts go to the workspace and come back past the XCDs' own caches (agent scope: sc1), 16 bytes at a
-// time, which the language's atomics do not offer.
-constexpr int kAgent = 16;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t parts_of(float *p, int floats) {
-    return __builtin_amdgcn_make_buffer_rsrc(p, 0, floats * 4, 0x00020000);
-}
-__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t r, int at, f32x4 v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at * 4, 0, kAgent);
-}
-__device__ __forceinline__ f32x4 load_part(__amdgpu_buffer_rsrc_t r, int at) {
-    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at * 4, 0, kAgent));
-}
-
-// A softmax's sums so far, and more of them.
-struct Sums {
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float top = kNoMax, sum = 0.0f;
-
-    __device__ __forceinline__ void add(f32x4 o2, float top2, float sum2) {
-        const float now = fmaxf(top, top2);
-        const float keep = exp2_of(top - now), more = exp2_of(top2 - now);
-        top = now;
-        sum = sum * keep + sum2 * more;
-        o = o * keep + o2 * more;
     }
 };
 
@@ -410,7 +295,10 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                     const Where q = where(a, r, head, x);
                     row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
                 }
-                const float t = load_query<BITS, D>(row, a.scale, lane, query + n * (D / 32) * 128);
+                half8 *words = query + n * (D / 32) * 128 + lane;
+                const float t = load_query<BITS, D>(row, a.scale, g, [&](int s, half8 hi, half8 lo) {
+                    words[2 * s * 64] = hi, words[(2 * s + 1) * 64] = lo;
+                });
                 if (g == 0) to_scores[x] = t;
             }
             w.top[n] = kNoMax;
@@ -430,11 +318,14 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                 const Seen seen = {t0 < all_lo || t0 + kTileTokens > all_hi, t0, lo, hi};
                 const bool there = __builtin_amdgcn_readlane(page, l) >= 0;
                 const uint8_t *next = tile_of(min(l + 1, mine - 1));
-                f32x4 s[NR][2];
-                if (there) w.scores(keys, query, lane, s);
+                f32x4 z[NR][2];
+                if (there) w.scores(keys, query, lane, z);
                 keys.load(next, g, col);
                 if (there) {
-                    w.weights(s, seen, g);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        weigh(z[n], seen.masked, t0, g, max(w.begin[n], lo), min(w.end[n], hi), w.to_score[n], w.top[n], w.sum[n],
+                              w.acc[n], w.p_hi[n], w.p_lo[n]);
                     w.add_values(values, seen, g);
                 }
                 values.load(next, g, col);
@@ -513,7 +404,7 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
 #pragma unroll
                             for (int j = 0; j < kAhead; ++j) {
                                 // (past the last one: past the buffer, nothing is read)
-                                const int at_part = (i + j) * f.slot | static_cast<int>(oob_bit(i + j < i1) >> 2);
+                                const uint32_t at_part = static_cast<uint32_t>((i + j) * f.slot) | oob_bit(i + j < i1) >> 2;
                                 st[j] = load_part(parts, at_part + (vecs + x) * 4);
                                 o[j] = load_part(parts, at_part + 4 * e);
                             }
@@ -566,23 +457,24 @@ hipError_t run(FewArgs f, hipStream_t stream) {
 
 template <int BITS, int D>
 hipError_t run_rows(const FewArgs &f, hipStream_t stream) {
-    return f.a.c.max_rows * f.a.group <= 16 ? run<BITS, D, 1>(f, stream) : run<BITS, D, 2>(f, stream);
+    if constexpr (few_rows(D) > 16)
+        if (f.a.c.max_rows * f.a.group > 16) return run<BITS, D, 2>(f, stream);
+    return run<BITS, D, 1>(f, stream);
 }
 
 int64_t most_pieces() { return int64_t(device_info().cus) * 3 * kPiecesPerSlot; }
-int64_t counter_bytes() { return (2 * most_pieces() * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
 int64_t few_workspace(int dim, const AttentionArgs &a) {
-    return counter_bytes() + 2 * most_pieces() * a.c.max_rows * a.group * (dim + 4) * 4;
+    return attention_counter_bytes() + 2 * most_pieces() * a.c.max_rows * a.group * (dim + 4) * 4;
 }
 
 hipError_t launch_few(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream) {
     FewArgs f = {};
     f.a = a;
     f.arrived = static_cast<uint32_t *>(workspace);
-    f.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + counter_bytes());
+    f.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + attention_counter_bytes());
     f.slot = a.c.max_rows * a.group * (dim + 4);
     if (bits == 4)
         return dim == 64 ? run_rows<4, 64>(f, stream) : dim == 128 ? run_rows<4, 128>(f, stream) : run_rows<4, 256>(f, stream);

@@ -118,12 +118,17 @@ __device__ __forceinline__ uint8_t *tile_at(const CacheArgs &c, int s, int t, in
 hipError_t launch_cache_append(int bits, int dim, const AppendArgs &a, hipStream_t stream);
 hipError_t launch_cache_read(int bits, int dim, const ReadArgs &a, hipStream_t stream);
 
-// Few rows a sequence and kv head: at most kFewRows.
-constexpr int kFewRows = 32;
+// The attention's workspace starts with counters, as many whatever the call, so that one workspace
+// serves every kernel; parts that are joined follow.
+constexpr int kCountersPerCu = 12;
+int64_t attention_counter_bytes();
+
+// Few rows a sequence and kv head: one or two operands of 16 columns (256 dimensions: one, for the registers).
+constexpr int few_rows(int dim) { return dim == 256 ? 16 : 32; }
 int64_t few_workspace(int dim, const AttentionArgs &a);
 hipError_t launch_few(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream);
-
-int64_t attention_workspace(int dim, const AttentionArgs &a);
-hipError_t launch_attention(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream);
+// Many rows.
+int64_t rows_workspace(int dim);
+hipError_t launch_rows(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream);
 
 }  // namespace q8

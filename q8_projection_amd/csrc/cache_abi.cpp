@@ -7,6 +7,7 @@
 
 #include "../../include/q8_cache.h"
 #include "cache.h"
+#include "launch.h"
 #include "ranges.h"
 
 namespace {
@@ -75,6 +76,10 @@ q8::CacheArgs args_of(const q8_cache *c, const q8_cache_batch *b) {
     return a;
 }
 
+bool few(const q8::AttentionArgs &a, int64_t dim) {
+    return int64_t(a.c.max_rows) * a.group <= q8::few_rows(static_cast<int>(dim));
+}
+
 q8::Range pool_range(const q8_cache *c) { return {c->data, c->pages * q8_cache_page_bytes(c)}; }
 
 // Whether `out` overlaps what a call reads beside its rows: the table, the lengths and the starts.
@@ -84,6 +89,8 @@ bool overlaps_batch(const q8::Range &out, const q8_cache_batch *b) {
 }
 
 }  // namespace
+
+int64_t q8::attention_counter_bytes() { return (int64_t(kCountersPerCu) * device_info().cus * 4 + 255) / 256 * 256; }
 
 extern "C" {
 
@@ -134,7 +141,7 @@ int64_t q8_attention_workspace_bytes(const q8_cache *cache, const q8_cache_batch
     a.c = args_of(cache, batch);
     a.heads = static_cast<int>(heads);
     a.group = a.heads / a.c.kv_heads;
-    return q8::attention_workspace(cache->head_dim, a);
+    return few(a, cache->head_dim) ? q8::few_workspace(cache->head_dim, a) : q8::rows_workspace(cache->head_dim);
 }
 
 q8_status q8_attention(const q8_cache *cache, const q8_cache_batch *batch, const float *q, int64_t q_ld,
@@ -167,9 +174,9 @@ q8_status q8_attention(const q8_cache *cache, const q8_cache_batch *batch, const
     a.window = static_cast<int>(window);
     a.out = out;
     a.lse = lse;
-    return q8::launch_attention(cache->bits, cache->head_dim, a, workspace, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
-               ? Q8_OK
-               : Q8_E_HIP;
+    const auto launch = few(a, cache->head_dim) ? q8::launch_few : q8::launch_rows;
+    return launch(cache->bits, cache->head_dim, a, workspace, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? Q8_OK
+                                                                                                                 : Q8_E_HIP;
 }
 
 }  // extern "C"
