@@ -245,7 +245,19 @@ template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t add_dpp(uint32_t v) {
     return v + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
 }
+__device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
+    return static_cast<int64_t>(static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(v >> 32), l)) << 32 |
+                                static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)));
+}
 // Inclusive sum over the lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int64_t up = __shfl_up(v, off, 64);
+        v += lane >= off ? up : 0;
+    }
+    return v;
+}
 __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     v = add_dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
     v = add_dpp<0x112, 0xf>(v);
@@ -258,25 +270,24 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
 }
 
-// Scores of 32 tokens (lane (g, c): row c, tokens 8 g + 4 i + r in s[i][r]) to weights in two words, with the
-// running maximum and sum of the softmax and the sums so far.  masked: only tokens t, t0 the first, of
-// [begin, end) are seen by the lane's row.
-template <int M, int N>
-__device__ __forceinline__ void weigh(const f32x4 (&s)[2], bool masked, int t0, int g, int begin, int end, float to_score,
-                                      float &top, float &sum, f32x4 (&acc)[M][N], half8 &hi, half8 &lo) {
-    float z[8];  // pairs (token p, token p + 4) of the lane's eight
+// Scores of 32 tokens: lane (g, c) has row c's of tokens 8 g + 4 i + r in s[i][r].  Those that the row does
+// not see (outside [begin, end), t0 the first token) become -inf.
+__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int t0, int g, int begin, int end) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) z[2 * p] = s[0][p], z[2 * p + 1] = s[1][p];
-    if (masked) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int t = t0 + 8 * g + (e >> 1) + 4 * (e & 1);
-            z[e] = t >= begin && t < end ? z[e] : -INFINITY;
+        for (int r = 0; r < 4; ++r) {
+            const int t = t0 + 8 * g + 4 * i + r;
+            s[i][r] = t >= begin && t < end ? s[i][r] : -INFINITY;
         }
-    }
-    float most = z[0];
+}
+
+// Keeps the softmax's maximum up to kMaxSlack below the scores' at most, and the sums in step with it.
+template <int M, int N>
+__device__ __forceinline__ void follow_max(const f32x4 (&s)[2], float to_score, float &top, float &sum, f32x4 (&acc)[M][N]) {
+    float most = s[0][0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) most = fmaxf(most, z[e]);
+    for (int e = 1; e < 8; ++e) most = fmaxf(most, s[e >> 2][e & 3]);
     most *= to_score;
     if (__any(most > top + kMaxSlack)) {
         const float now = fmaxf(column_max(most), top);
@@ -288,11 +299,15 @@ __device__ __forceinline__ void weigh(const f32x4 (&s)[2], bool masked, int t0, 
 #pragma unroll
             for (int w = 0; w < N; ++w) acc[m][w] *= keep;
     }
+}
+
+// Scores to weights in two words, pairs (token p, token p + 4) of the lane's eight, and to their sum.
+__device__ __forceinline__ void weights_of(const f32x4 (&s)[2], float to_score, float top, float &sum, half8 &hi, half8 &lo) {
     const float below = kWeightShift - top;
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        w[e] = exp2_of(__builtin_fmaf(z[e], to_score, below));
+        w[e] = exp2_of(__builtin_fmaf(s[e & 1][e >> 1], to_score, below));
         sum += w[e];
     }
     two_words(w, hi, lo);

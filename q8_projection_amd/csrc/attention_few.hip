@@ -192,9 +192,9 @@ struct Pieces {
                 const int64_t before = pieces + (l ? int64_t(lane_of(scan, l - 1)) * a.c.kv_heads : 0);
                 out.s = s0 + l;
                 out.n = static_cast<int>(lane_of(count, l));
-                out.rows = Rows{static_cast<int>(lane_of(rows.first, l)), static_cast<int>(lane_of(rows.n, l)),
-                                static_cast<int>(lane_of(rows.at, l)), static_cast<int>(lane_of(rows.end, l))};
-                out.span = Span{static_cast<int>(lane_of(span.first, l)), static_cast<int>(lane_of(span.n, l))};
+                const auto at = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+                out.rows = Rows{at(rows.first), at(rows.n), at(rows.at), at(rows.end)};
+                out.span = Span{at(span.first), at(span.n)};
                 const int rest = static_cast<int>(p - before);
                 out.head = rest / out.n;
                 out.index = rest - out.head * out.n;
@@ -323,9 +323,11 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                 keys.load(next, g, col);
                 if (there) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        weigh(z[n], seen.masked, t0, g, max(w.begin[n], lo), min(w.end[n], hi), w.to_score[n], w.top[n], w.sum[n],
-                              w.acc[n], w.p_hi[n], w.p_lo[n]);
+                    for (int n = 0; n < NR; ++n) {
+                        if (seen.masked) mask_scores(z[n], t0, g, max(w.begin[n], lo), min(w.end[n], hi));
+                        follow_max(z[n], w.to_score[n], w.top[n], w.sum[n], w.acc[n]);
+                        weights_of(z[n], w.to_score[n], w.top[n], w.sum[n], w.p_hi[n], w.p_lo[n]);
+                    }
                     w.add_values(values, seen, g);
                 }
                 values.load(next, g, col);
