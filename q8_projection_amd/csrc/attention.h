@@ -98,19 +98,20 @@ __device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Eight f32 as two binary16 words.  (The empty asms make the pair one value, which else is converted half by
+// Two f32 as two binary16 words each.  (The empty asms make the pair one value, which else is converted half by
 // half once more for the difference, and hide the factor: a mixed multiply-add takes the words as they are.)
-__device__ __forceinline__ void two_words(const float (&x)[8], half8 &hi, half8 &lo) {
-    half2 h[4], l[4];
+__device__ __forceinline__ void two_words(float x, float y, half2 &hi, half2 &lo) {
     float minus = -1.0f;
     asm("" : "+s"(minus));
+    hi = half2{static_cast<_Float16>(x), static_cast<_Float16>(y)};
+    asm("" : "+v"(hi));
+    lo = half2{static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi.x), minus, x)),
+               static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi.y), minus, y))};
+}
+__device__ __forceinline__ void two_words(const float (&x)[8], half8 &hi, half8 &lo) {
+    half2 h[4], l[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        h[p] = half2{static_cast<_Float16>(x[2 * p]), static_cast<_Float16>(x[2 * p + 1])};
-        asm("" : "+v"(h[p]));
-        l[p] = half2{static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h[p].x), minus, x[2 * p])),
-                     static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h[p].y), minus, x[2 * p + 1]))};
-    }
+    for (int p = 0; p < 4; ++p) two_words(x[2 * p], x[2 * p + 1], h[p], l[p]);
     hi = join(h[0], h[1], h[2], h[3]);
     lo = join(l[0], l[1], l[2], l[3]);
 }
@@ -206,22 +207,22 @@ struct Out {
     static __device__ __forceinline__ int out_dim(int c, int m, int w) { return unit(c) * kUnit + 16 * w + chunk(c, m); }
 
     // fn(first dimension, four values) for lane group g's part of a row's sums.
-    template <typename Fn>
-    static __device__ __forceinline__ void for_each_vec(const f32x4 (&acc)[kChunks][kIn], int g, Fn fn) {
+    template <typename Acc, typename Fn>
+    static __device__ __forceinline__ void for_each_vec(Acc acc, int g, Fn fn) {
 #pragma unroll
         for (int w = 0; w < kIn; ++w) {
             if constexpr (kChunks == 1) {
-                fn(out_dim(4 * g, 0, w), acc[0][w]);
+                fn(out_dim(4 * g, 0, w), acc(0, w));
             } else if constexpr (kChunks == 2) {
 #pragma unroll
                 for (int r = 0; r < 4; r += 2)
-                    fn(out_dim(4 * g + r, 0, w), f32x4{acc[0][w][r], acc[1][w][r], acc[0][w][r + 1], acc[1][w][r + 1]});
+                    fn(out_dim(4 * g + r, 0, w), f32x4{acc(0, w)[r], acc(1, w)[r], acc(0, w)[r + 1], acc(1, w)[r + 1]});
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int m = 0; m < kChunks; m += 4)
-                        fn(out_dim(4 * g + r, m, w), f32x4{acc[m][w][r], acc[m + 1][w][r], acc[m + 2][w][r], acc[m + 3][w][r]});
+                        fn(out_dim(4 * g + r, m, w), f32x4{acc(m, w)[r], acc(m + 1, w)[r], acc(m + 2, w)[r], acc(m + 3, w)[r]});
             }
         }
     }
@@ -282,35 +283,45 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int t0, int g, int be
         }
 }
 
-// Keeps the softmax's maximum up to kMaxSlack below the scores' at most, and the sums in step with it.
-template <int M, int N>
-__device__ __forceinline__ void follow_max(const f32x4 (&s)[2], float to_score, float &top, float &sum, f32x4 (&acc)[M][N]) {
+__device__ __forceinline__ float largest(const f32x4 (&s)[2]) {
     float most = s[0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) most = fmaxf(most, s[e >> 2][e & 3]);
-    most *= to_score;
+    return most;
+}
+
+// Keeps the softmax's maximum at most kMaxSlack below `most`, the lane's largest score, and the sums in step
+// with it.
+// (acc(m, w): operand w of chunk m)
+template <typename O, typename Acc>
+__device__ __forceinline__ void follow_max(float most, float &top, float &sum, Acc acc) {
     if (__any(most > top + kMaxSlack)) {
         const float now = fmaxf(column_max(most), top);
         const float keep = exp2_of(top - now);
         top = now;
         sum *= keep;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+        for (int m = 0; m < O::kChunks; ++m)
 #pragma unroll
-            for (int w = 0; w < N; ++w) acc[m][w] *= keep;
+            for (int w = 0; w < O::kIn; ++w) acc(m, w) *= keep;
     }
 }
 
-// Scores to weights in two words, pairs (token p, token p + 4) of the lane's eight, and to their sum.
-__device__ __forceinline__ void weights_of(const f32x4 (&s)[2], float to_score, float top, float &sum, half8 &hi, half8 &lo) {
+// Scores to weights in two words, a pair (token p, token p + 4) of the lane's eight at a time, and to
+// their sum.
+__device__ __forceinline__ void weigh_pair(const f32x4 (&s)[2], int p, float to_score, float top, float &sum, half2 &hi, half2 &lo) {
     const float below = kWeightShift - top;
-    float w[8];
+    const float x = exp2_of(__builtin_fmaf(s[0][p], to_score, below)), y = exp2_of(__builtin_fmaf(s[1][p], to_score, below));
+    sum += x;
+    sum += y;
+    two_words(x, y, hi, lo);
+}
+__device__ __forceinline__ void weights_of(const f32x4 (&s)[2], float to_score, float top, float &sum, half8 &hi, half8 &lo) {
+    half2 h[4], l[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        w[e] = exp2_of(__builtin_fmaf(s[e & 1][e >> 1], to_score, below));
-        sum += w[e];
-    }
-    two_words(w, hi, lo);
+    for (int p = 0; p < 4; ++p) weigh_pair(s, p, to_score, top, sum, h[p], l[p]);
+    hi = join(h[0], h[1], h[2], h[3]);
+    lo = join(l[0], l[1], l[2], l[3]);
 }
 
 // Row x of a sequence and kv head: which of the call's.

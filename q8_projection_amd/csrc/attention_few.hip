@@ -325,7 +325,7 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         if (seen.masked) mask_scores(z[n], t0, g, max(w.begin[n], lo), min(w.end[n], hi));
-                        follow_max(z[n], w.to_score[n], w.top[n], w.sum[n], w.acc[n]);
+                        follow_max<O>(largest(z[n]) * w.to_score[n], w.top[n], w.sum[n], [&](int m, int j) -> f32x4 & { return w.acc[n][m][j]; });
                         weights_of(z[n], w.to_score[n], w.top[n], w.sum[n], w.p_hi[n], w.p_lo[n]);
                     }
                     w.add_values(values, seen, g);
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
 #pragma unroll
             for (int v = 1; v < WAVES; ++v) top = fmaxf(top, tops[v][n * 16 + col]);
             const float scale = exp2_of(w.top[n] - top) * Scales<BITS>::kUp;
-            if (n * 16 + col < rows) O::for_each_vec(w.acc[n], g, [&](int dim, f32x4 v) {
+            if (n * 16 + col < rows) O::for_each_vec([&](int m, int j) { return w.acc[n][m][j]; }, g, [&](int dim, f32x4 v) {
                 *reinterpret_cast<f32x4 *>(meet + (wid * 16 + col) * kPad + dim) = v * scale;
             });
             __syncthreads();

@@ -151,19 +151,14 @@ struct KeyCodes {
         for (int u = 0; u < kWords; ++u)
             w[u] = *reinterpret_cast<const uint32_t *>(tile + u * 8 + T::kKeyWords + (c * T::kBlocks + block) * 4);
     }
-    // to [half][step][lane]
-    __device__ __forceinline__ void store(half8 *keys, int wid, int lane) const {
-        Scales<BITS> sc[kWords];
-#pragma unroll
-        for (int u = 0; u < kWords; ++u) sc[u].set(__builtin_amdgcn_perm(w[u], w[u], wid >> 1 ? 0x03020302u : 0x01000100u));
-#pragma unroll
-        for (int e = 0; e < kOperands; ++e) {
-            half8 v;
-            const Scales<BITS> &s = sc[e * kWords / kOperands];
-            if constexpr (BITS == 4) v = values_of(x[e], s, s, s, s);
-            else v = values_of(x[2 * e], x[2 * e + 1], s, s, s, s);
-            keys[((wid >> 1) * (D / 32) + (wid & 1) * kOperands + e) * 64 + lane] = v;
-        }
+    // operand e to [half][step][lane]
+    __device__ __forceinline__ void store(half8 *keys, int e, int wid, int lane) const {
+        Scales<BITS> s;
+        s.set(__builtin_amdgcn_perm(w[e * kWords / kOperands], w[e * kWords / kOperands], wid >> 1 ? 0x03020302u : 0x01000100u));
+        half8 v;
+        if constexpr (BITS == 4) v = values_of(x[e], s, s, s, s);
+        else v = values_of(x[2 * e], x[2 * e + 1], s, s, s, s);
+        keys[((wid >> 1) * (D / 32) + (wid & 1) * kOperands + e) * 64 + lane] = v;
     }
 };
 
@@ -198,21 +193,15 @@ struct ValueCodes {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) w[b] = *reinterpret_cast<const u32x4 *>(tile + b * 64 + T::kValueWords + (block * 4 + g) * 16);
     }
-    // to [operand][lane]; there: the halves of a pair of words whose tokens are there
-    __device__ __forceinline__ void store(half8 *values, const uint32_t (&there)[4], int wid, int lane) const {
-        Scales<BITS> sc[kBlocks][4];
+    // operand e to [operand][lane]
+    __device__ __forceinline__ void store(half8 *values, int e, int wid, int lane) const {
+        Scales<BITS> s[4];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int p = 0; p < 4; ++p) sc[b][p].set(w[b][p] & there[p]);
-#pragma unroll
-        for (int e = 0; e < kOperands; ++e) {
-            const Scales<BITS>(&s)[4] = sc[kBlocks == 2 ? e / 2 : 0];
-            half8 v;
-            if constexpr (BITS == 4) v = values_of(x[e], s[0], s[1], s[2], s[3]);
-            else v = values_of(x[2 * e], x[2 * e + 1], s[0], s[1], s[2], s[3]);
-            values[(wid * kOperands + e) * 64 + lane] = v;
-        }
+        for (int p = 0; p < 4; ++p) s[p].set(w[kBlocks == 2 ? e / 2 : 0][p]);
+        half8 v;
+        if constexpr (BITS == 4) v = values_of(x[e], s[0], s[1], s[2], s[3]);
+        else v = values_of(x[2 * e], x[2 * e + 1], s[0], s[1], s[2], s[3]);
+        values[(wid * kOperands + e) * 64 + lane] = v;
     }
 };
 
@@ -261,64 +250,54 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
             const int lo = a.window ? max(tile_rows.at - a.window + 1, 0) : 0, hi = min(tile_rows.at + tile_rows.n, r.end);
             const int all_lo = a.window ? max(tile_rows.at + tile_rows.n - a.window, 0) : 0, all_hi = min(tile_rows.at + 1, r.end);
 
-            // Pages of 64 tiles at a time, one a lane.
+            // Pages of the tiles paged .. paged + 63, one a lane (-1: none).
             const int shift = c.page_shift - 5;
-            int paged = 0, page = -1;
-            const auto page_of = [&](int tile) {  // -1: none
-                if (tile >= to) return -1;
-                if (tile < paged || tile >= paged + 64 || tile == from) {
-                    paged = tile;
-                    const int t = span.first + tile + lane;
-                    page = -1;
-                    if (tile + lane < to && t * kTileTokens < hi) page = c.table[it.s * c.table_ld + (t >> shift)];
-                    if (page < 0 || page >= c.pages) page = -1;
-                }
-                return __builtin_amdgcn_readlane(page, tile - paged);
+            int paged, page;
+            const auto look_up = [&](int tile) {
+                paged = tile;
+                const int t = span.first + tile + lane;
+                page = -1;
+                if (tile + lane < to && t * kTileTokens < hi) page = c.table[it.s * c.table_ld + (t >> shift)];
+                if (page < 0 || page >= c.pages) page = -1;
             };
-            const auto tile_at_page = [&](int tile, int pg) -> const uint8_t * {  // (none: the pool's first, not looked at)
+            const auto page_of = [&](int tile) { return __builtin_amdgcn_readlane(page, tile - paged); };
+            const auto tile_in = [&](int tile, int pg) -> const uint8_t * {  // (none: the pool's first, not looked at)
                 const int t = span.first + tile;
                 return c.data + (((int64_t(max(pg, 0)) * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes;
-            };
-            // tokens of a tile that are there: what a pair of value words keeps
-            const auto store_values = [&](const ValueCodes<BITS, D> &v, int tile, int pg) {
-                const int t0 = (span.first + tile) * kTileTokens;
-                uint32_t there[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                if (pg < 0 || t0 < lo || t0 + kTileTokens > hi) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int t = t0 + 8 * g + q;
-                        there[q] = pg < 0 ? 0u
-                                          : (t >= lo && t < hi ? 0xffffu : 0u) | (t + 4 >= lo && t + 4 < hi ? 0xffff0000u : 0u);
-                    }
-                }
-                v.store(values[tile & 1], there, wid, lane);
             };
 
             KeyCodes<BITS, D> kc;
             ValueCodes<BITS, D> vc;
-            // pages of the tiles whose scores, and whose codes, come next
-            int pages[4];
+            // the value words of tokens that are not there are no value's
+            const auto clear_words = [&](int tile, int pg) {
+                const int t0 = (span.first + tile) * kTileTokens;
+                if (pg >= 0 && t0 >= lo && t0 + kTileTokens <= hi) return;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) pages[i] = page_of(from + i);
-            kc.load(tile_at_page(from, pages[0]), wid, g, col);
-            vc.load(tile_at_page(from, pages[0]), wid, g, col);
+                for (int q = 0; q < 4; ++q) {
+                    const int t = t0 + 8 * g + q;
+                    const uint32_t there = (t >= lo && t < hi ? 0xffffu : 0u) | (t + 4 >= lo && t + 4 < hi ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (auto &w : vc.w) w[q] = pg < 0 ? 0u : w[q] & there;
+                }
+            };
+            look_up(from);
+            // pages of tile + 1, tile + 2
+            int page1 = page_of(from + 1), page2 = page_of(from + 2);
+            const int page0 = page_of(from);
+            kc.load(tile_in(from, page0), wid, g, col);
+            vc.load(tile_in(from, page0), wid, g, col);
 
             half8 q_hi[NR][kSteps], q_lo[NR][kSteps];
             float to_score[NR], top[NR], sum[NR];
-            int begin[NR], end[NR];
-            f32x4 acc[NR][O::kChunks][O::kIn];
+            f32x4 acc[O::kChunks][O::kIn][NR];  // row operands last
             const int first_row = row0 + wid * 16 * NR;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const int x = first_row + n * 16 + col;
                 const float *row = nullptr;
-                begin[n] = end[n] = 0;
                 if (x < rows) {
                     const Where q = where(a, r, head, x);
                     row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
-                    const int t = r.at + x / a.group;
-                    begin[n] = a.window ? max(t - a.window + 1, 0) : 0;
-                    end[n] = min(t + 1, r.end);
                 }
                 to_score[n] = load_query<BITS, D>(row, a.scale, g, [&](int s, half8 h, half8 l) { q_hi[n][s] = h, q_lo[n][s] = l; });
                 top[n] = kNoMax;
@@ -326,7 +305,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
 #pragma unroll
                 for (int m = 0; m < O::kChunks; ++m)
 #pragma unroll
-                    for (int j = 0; j < O::kIn; ++j) acc[n][m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int j = 0; j < O::kIn; ++j) acc[m][j][n] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
 
             const auto scores = [&](int tile, f32x4(&z)[NR][2]) {
@@ -342,52 +321,102 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
                     for (int n = 0; n < NR; ++n) z[n][0] = mfma(k0, q_lo[n][s], z[n][0]), z[n][1] = mfma(k1, q_lo[n][s], z[n][1]);
                 }
             };
-            const auto mask = [&](int tile, int pg, f32x4(&z)[NR][2]) {
+            // What a row does not see of a tile, and the maximum.
+            const auto settle = [&](int tile, int pg, f32x4(&z)[NR][2], float (&most)[NR]) {
                 const int t0 = (span.first + tile) * kTileTokens;
-                if (pg < 0 || t0 < all_lo || t0 + kTileTokens > all_hi)
+                if (pg < 0 || t0 < all_lo || t0 + kTileTokens > all_hi) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) mask_scores(z[n], t0, g, begin[n], pg < 0 ? 0 : end[n]);
+                    for (int n = 0; n < NR; ++n) {
+                        const int x = first_row + n * 16 + col, t = r.at + x / a.group;
+                        const int end = pg < 0 || x >= rows ? 0 : min(t + 1, r.end);
+                        mask_scores(z[n], t0, g, a.window ? t - a.window + 1 : 0, end);
+                        most[n] = largest(z[n]);
+                    }
+                }
 #pragma unroll
-                for (int n = 0; n < NR; ++n) follow_max(z[n], to_score[n], top[n], sum[n], acc[n]);
+                for (int n = 0; n < NR; ++n) follow_max<O>(most[n] * to_score[n], top[n], sum[n], [&](int m, int j) -> f32x4 & { return acc[m][j][n]; });
             };
 
             // keys of the first two tiles, values of the first
-            kc.store(keys[from & 1], wid, lane);
-            store_values(vc, from, pages[0]);
-            kc.load(tile_at_page(from + 1, pages[1]), wid, g, col);
-            vc.load(tile_at_page(from + 1, pages[1]), wid, g, col);
-            kc.store(keys[(from + 1) & 1], wid, lane);
-            kc.load(tile_at_page(from + 2, pages[2]), wid, g, col);
+            constexpr int kMine = D / 64;  // operands of keys, and of values, that a wave makes
+            clear_words(from, page0);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) kc.store(keys[from & 1], e, wid, lane), vc.store(values[from & 1], e, wid, lane);
+            kc.load(tile_in(from + 1, page1), wid, g, col);
+            vc.load(tile_in(from + 1, page1), wid, g, col);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) kc.store(keys[(from + 1) & 1], e, wid, lane);
+            kc.load(tile_in(from + 2, page2), wid, g, col);
+            clear_words(from + 1, page1);
             __syncthreads();
             f32x4 z[NR][2];
+            float most[NR];
             if (from < to) {
                 scores(from, z);
-                mask(from, pages[0], z);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) most[n] = largest(z[n]);
+                settle(from, page0, z, most);
             }
             __syncthreads();
             for (int tile = from; tile < to; ++tile) {
-                half8 p_hi[NR], p_lo[NR];
+                if (tile + 3 - paged > 63) look_up(tile);
+                const int page3 = page_of(tile + 3);
+                // The weights of this tile beside the scores of the next.  The order of the steps is kept (the
+                // barriers), for the compiler makes all weights and then all products.
+                half2 p_hi[NR][4], p_lo[NR][4];
+                f32x4 next[NR][2];
 #pragma unroll
-                for (int n = 0; n < NR; ++n) weights_of(z[n], to_score[n], top[n], sum[n], p_hi[n], p_lo[n]);
-                scores(tile + 1, z);
-                pages[3] = page_of(tile + 3);
-                kc.store(keys[tile & 1], wid, lane);
-                store_values(vc, tile + 1, pages[1]);
-                kc.load(tile_at_page(tile + 3, pages[3]), wid, g, col);
-                vc.load(tile_at_page(tile + 2, pages[2]), wid, g, col);
-                const half8 *v = values[tile & 1] + lane;
+                for (int n = 0; n < NR; ++n) next[n][0] = next[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                const half8 *k = keys[(tile + 1) & 1] + lane, *v = values[tile & 1] + lane;
+                half8 k0 = k[0], k1 = k[kSteps * 64], k0_next = k0, k1_next = k1;
+                half8 x = v[0], x_next = x;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int m = 0; m < O::kChunks; ++m)
+                for (int s = 0; s < 2 * kSteps; ++s) {
+                    if (s % 2 == 0 && s / 2 + 1 < kSteps) k0_next = k[(s / 2 + 1) * 64], k1_next = k[(kSteps + s / 2 + 1) * 64];
 #pragma unroll
-                    for (int w = 0; w < O::kIn; ++w) {
-                        const half8 x = v[(m * O::kIn + w) * 64];
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) acc[n][m][w] = mfma(x, p_hi[n], acc[n][m][w]);
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) acc[n][m][w] = mfma(x, p_lo[n], acc[n][m][w]);
+                    for (int n = 0; n < NR; ++n) {
+                        const half8 q = s % 2 ? q_lo[n][s / 2] : q_hi[n][s / 2];
+                        next[n][0] = mfma(k0, q, next[n][0]);
+                        next[n][1] = mfma(k1, q, next[n][1]);
                     }
-                if (tile + 1 < to) mask(tile + 1, pages[1], z);
-                pages[1] = pages[2], pages[2] = pages[3];
+#pragma unroll
+                    for (int i = s * 4 * NR / (2 * kSteps); i < (s + 1) * 4 * NR / (2 * kSteps); ++i)
+                        weigh_pair(z[i / 4], i % 4, to_score[i / 4], top[i / 4], sum[i / 4], p_hi[i / 4][i % 4], p_lo[i / 4][i % 4]);
+                    if (s % 2) k0 = k0_next, k1 = k1_next;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                half8 w_hi[NR], w_lo[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    w_hi[n] = join(p_hi[n][0], p_hi[n][1], p_hi[n][2], p_hi[n][3]);
+                    w_lo[n] = join(p_lo[n][0], p_lo[n][1], p_lo[n][2], p_lo[n][3]);
+                    z[n][0] = next[n][0], z[n][1] = next[n][1];
+                }
+                // The sums of this tile beside the next operands.
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    if (j + 1 < D / 16) x_next = v[(j + 1) * 64];
+                    f32x4(&o)[NR] = acc[j / O::kIn][j % O::kIn];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) o[n] = mfma(x, w_hi[n], o[n]);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) o[n] = mfma(x, w_lo[n], o[n]);
+                    constexpr int kWork = 2 * kMine + NR;
+#pragma unroll
+                    for (int i = j * kWork / (D / 16); i < (j + 1) * kWork / (D / 16); ++i) {
+                        if (i < kMine) kc.store(keys[tile & 1], i, wid, lane);
+                        if (i == kMine - 1) kc.load(tile_in(tile + 3, page3), wid, g, col);
+                        if (i >= kMine && i < 2 * kMine) vc.store(values[(tile + 1) & 1], i - kMine, wid, lane);
+                        if (i == 2 * kMine - 1) vc.load(tile_in(tile + 2, page2), wid, g, col);
+                        if (i >= 2 * kMine) most[i - 2 * kMine] = largest(z[i - 2 * kMine]);
+                    }
+                    x = x_next;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (tile + 1 < to) settle(tile + 1, page1, z, most);
+                clear_words(tile + 2, page2);
+                page1 = page2, page2 = page3;
                 __syncthreads();
             }
 
@@ -404,10 +433,10 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
                 constexpr float kScale = Scales<BITS>::kUp;
                 if (alone) {
                     const Where to_row = where(a, r, head, x);
-                    O::for_each_vec(acc[n], g, [&](int dim, f32x4 o) { write_row<D>(a, to_row, dim, o * kScale, total, top[n]); });
+                    O::for_each_vec([&](int m, int j) { return acc[m][j][n]; }, g, [&](int dim, f32x4 o) { write_row<D>(a, to_row, dim, o * kScale, total, top[n]); });
                 } else {
                     const int y = x - row0;
-                    O::for_each_vec(acc[n], g, [&](int dim, f32x4 o) { store_part(parts, mine + y * D + dim, o * kScale); });
+                    O::for_each_vec([&](int m, int j) { return acc[m][j][n]; }, g, [&](int dim, f32x4 o) { store_part(parts, mine + y * D + dim, o * kScale); });
                     if (g == 0) store_part(parts, mine + kTile * D + 4 * y, f32x4{top[n], total, 0.f, 0.f});
                 }
             }
