@@ -6,15 +6,10 @@
 // hi = rne16(x), lo = rne16(x - hi): 22 bits or more of it.  Both words go through the matrix
 // cores into the same f32 sums.
 //
-// v_mfma_f32_16x16x32_f16, as its lanes hold it (lane = 16 g + c):
-//   A: row c, depth 8 g + e (e = 0 .. 7);  B: column c, depth 8 g + e;  C: column c, rows 4 g + r
-// A product's depth may be taken in any order, if both operands take the same.
-//   scores: A = keys (row c of half i is token 8 (c / 4) + 4 i + c % 4 of the tile), B = queries
-//     (column c is row c of the workgroup's), depth = dimensions.  Lane (g, c) gets row c's scores
-//     of the tokens 8 g + 4 i + r, i = 0, 1.
-//   output: A = values (row c is a dimension), B = weights, depth = tokens: lane (g, c) gives the
-//     weights of tokens 8 g .. 8 g + 7 to row c, which are the ones it has just computed.
-// So scores turn into weights without leaving their lane.
+// A product's depth may be taken in any order, if both operands take the same, and rows in any: scores are
+// made with keys as rows and queries as columns, sums with the values' dimensions as rows and weights as
+// columns, and the tokens are put on the scores' rows such that a lane's scores are the weights that it
+// gives to the sums.  So scores turn into weights without leaving their lane.
 #pragma once
 
 #include "cache.h"
@@ -25,6 +20,7 @@ namespace q8 {
 using half2 = _Float16 __attribute__((ext_vector_type(2)));
 using half8 = _Float16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -97,6 +93,9 @@ __device__ __forceinline__ half8 values_of(uint32_t x, uint32_t y, const Scales<
 __device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ f32x16 mfma(half8 a, half8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
 
 // Two f32 as two binary16 words each.  (The empty asms make the pair one value, which else is converted half by
 // half once more for the difference, and hide the factor: a mixed multiply-add takes the words as they are.)
@@ -116,8 +115,8 @@ __device__ __forceinline__ void two_words(const float (&x)[8], half8 &hi, half8 
     lo = join(l[0], l[1], l[2], l[3]);
 }
 
-// The largest, and the sum, over the four lanes l % 16 + 16 g.  (A swap of a register with its copy
-// leaves a lane's own value in one of them and its partner's in the other.)
+// A lane's value and its partner's, 32 or 16 lanes away (a swap of a register with its copy leaves the one in the
+// first and the other in the second).
 __device__ __forceinline__ float2 lane_pair32(float v) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
     const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
@@ -130,24 +129,7 @@ __device__ __forceinline__ float2 lane_pair16(float v) {
     const uint32_t x = r[0], y = r[1];
     return make_float2(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
 }
-__device__ __forceinline__ float column_max(float v) {
-    const float2 a = lane_pair32(v), b = lane_pair16(fmaxf(a.x, a.y));
-    return fmaxf(b.x, b.y);
-}
-__device__ __forceinline__ float column_sum(float v) {
-    const float2 a = lane_pair32(v), b = lane_pair16(a.x + a.y);
-    return b.x + b.y;
-}
-
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
-
-// The first dimension of the eight that step s of a score's product takes in lane group g; a lane's
-// codes lie together, up to 16 bytes.
-template <int BITS, int D>
-__device__ __forceinline__ constexpr int key_dims(int s, int g) {
-    if (BITS == 8) return 64 * (s / 2) + 16 * g + 8 * (s % 2);
-    return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s % 4);
-}
 
 // A power of two that brings values of up to `most` into [2^14, 2^15) (small ones below), as its f32
 // exponent field.
@@ -157,17 +139,18 @@ __device__ __forceinline__ uint32_t lift_of(float most) {
 }
 
 // A query row as B operands of the scores' products: q * scale * log2(e), lifted, out(step, hi, lo) for
-// each step.  The row is lane column c's (null: none, zeros).  Returns what a score is multiplied by:
-// a power of two.
-template <int BITS, int D, typename Fn>
-__device__ __forceinline__ float load_query(const float *row, float scale, int g, Fn out) {
-    float x[D / 32][8];
+// each of STEPS.  The row is the lane's column's (null: none, zeros); dims(step) is the first of the eight
+// dimensions that the lane has of a step, column_max the largest over a column's lanes.  Returns what a
+// score is multiplied by: a power of two.
+template <int BITS, int STEPS, typename Dims, typename Max, typename Fn>
+__device__ __forceinline__ float load_query(const float *row, float scale, Dims dims, Max column_max, Fn out) {
+    float x[STEPS][8];
     float most = 0.0f;
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
         if (row) {
-            const float4 *p = reinterpret_cast<const float4 *>(row + key_dims<BITS, D>(s, g));
+            const float4 *p = reinterpret_cast<const float4 *>(row + dims(s));
             a = p[0], b = p[1];
         }
         const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -181,7 +164,7 @@ __device__ __forceinline__ float load_query(const float *row, float scale, int g
     const uint32_t lift = lift_of(column_max(most));
     const float f = __builtin_bit_cast(float, lift);
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[s][e] *= f;
         half8 hi, lo;
@@ -190,43 +173,6 @@ __device__ __forceinline__ float load_query(const float *row, float scale, int g
     }
     return __builtin_bit_cast(float, (254u << 23) - lift) * Scales<BITS>::kUp;
 }
-
-// The dimensions of the output's products.  A lane's value codes come as kChunks 16-byte chunks of
-// the layout, kIn operands each.  Row c of operand (m, w) is dimension out_dim(c, m, w): with a
-// lane's chunks side by side, its dimensions lie in 2 (4 bits) or 1 blocks, and it needs the words of those alone.
-template <int BITS, int D>
-struct Out {
-    static constexpr int kChunks = BITS == 4 ? D / 64 : D / 32;
-    static constexpr int kIn = BITS == 4 ? 4 : 2;
-    static constexpr int kBlocks = BITS == 4 ? 2 : 1;
-    static constexpr int kPer = 16 / kChunks;  // rows of one unit of the layout
-    static constexpr int kUnit = BITS == 4 ? 64 : 32;  // dimensions of it
-
-    static __device__ __forceinline__ int unit(int c) { return c / kPer; }
-    static __device__ __forceinline__ int chunk(int c, int m) { return c % kPer * kChunks + m; }
-    static __device__ __forceinline__ int out_dim(int c, int m, int w) { return unit(c) * kUnit + 16 * w + chunk(c, m); }
-
-    // fn(first dimension, four values) for lane group g's part of a row's sums.
-    template <typename Acc, typename Fn>
-    static __device__ __forceinline__ void for_each_vec(Acc acc, int g, Fn fn) {
-#pragma unroll
-        for (int w = 0; w < kIn; ++w) {
-            if constexpr (kChunks == 1) {
-                fn(out_dim(4 * g, 0, w), acc(0, w));
-            } else if constexpr (kChunks == 2) {
-#pragma unroll
-                for (int r = 0; r < 4; r += 2)
-                    fn(out_dim(4 * g + r, 0, w), f32x4{acc(0, w)[r], acc(1, w)[r], acc(0, w)[r + 1], acc(1, w)[r + 1]});
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int m = 0; m < kChunks; m += 4)
-                        fn(out_dim(4 * g + r, m, w), f32x4{acc(m, w)[r], acc(m + 1, w)[r], acc(m + 2, w)[r], acc(m + 3, w)[r]});
-            }
-        }
-    }
-};
 
 // Tiles that sequence s's rows see, [first, first + n).  A sequence without any keeps one, which
 // has no token, so that its rows are written; one without rows has none.
@@ -271,57 +217,26 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
 }
 
-// Scores of 32 tokens: lane (g, c) has row c's of tokens 8 g + 4 i + r in s[i][r].  Those that the row does
-// not see (outside [begin, end), t0 the first token) become -inf.
-__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int t0, int g, int begin, int end) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = t0 + 8 * g + 4 * i + r;
-            s[i][r] = t >= begin && t < end ? s[i][r] : -INFINITY;
-        }
-}
-
-__device__ __forceinline__ float largest(const f32x4 (&s)[2]) {
-    float most = s[0][0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) most = fmaxf(most, s[e >> 2][e & 3]);
-    return most;
-}
-
 // Keeps the softmax's maximum at most kMaxSlack below `most`, the lane's largest score, and the sums in step
-// with it.
-// (acc(m, w): operand w of chunk m)
-template <typename O, typename Acc>
-__device__ __forceinline__ void follow_max(float most, float &top, float &sum, Acc acc) {
+// with it: rescale(factor) multiplies the others.
+template <typename Max, typename Fn>
+__device__ __forceinline__ void follow_max(float most, float &top, float &sum, Max column_max, Fn rescale) {
     if (__any(most > top + kMaxSlack)) {
         const float now = fmaxf(column_max(most), top);
         const float keep = exp2_of(top - now);
         top = now;
         sum *= keep;
-#pragma unroll
-        for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-            for (int w = 0; w < O::kIn; ++w) acc(m, w) *= keep;
+        rescale(keep);
     }
 }
 
-// Scores to weights in two words, a pair (token p, token p + 4) of the lane's eight at a time, and to
-// their sum.
-__device__ __forceinline__ void weigh_pair(const f32x4 (&s)[2], int p, float to_score, float top, float &sum, half2 &hi, half2 &lo) {
+// Two scores to weights in two words, and to their sum.
+__device__ __forceinline__ void weigh_pair(float s, float t, float to_score, float top, float &sum, half2 &hi, half2 &lo) {
     const float below = kWeightShift - top;
-    const float x = exp2_of(__builtin_fmaf(s[0][p], to_score, below)), y = exp2_of(__builtin_fmaf(s[1][p], to_score, below));
+    const float x = exp2_of(__builtin_fmaf(s, to_score, below)), y = exp2_of(__builtin_fmaf(t, to_score, below));
     sum += x;
     sum += y;
     two_words(x, y, hi, lo);
-}
-__device__ __forceinline__ void weights_of(const f32x4 (&s)[2], float to_score, float top, float &sum, half8 &hi, half8 &lo) {
-    half2 h[4], l[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) weigh_pair(s, p, to_score, top, sum, h[p], l[p]);
-    hi = join(h[0], h[1], h[2], h[3]);
-    lo = join(l[0], l[1], l[2], l[3]);
 }
 
 // Row x of a sequence and kv head: which of the call's.
@@ -342,12 +257,25 @@ __device__ __forceinline__ void write_row(const AttentionArgs &a, const Where &a
         a.lse[at.row * a.heads + at.head] = total > 0 ? (top - kWeightShift) * kLn2 + logf(total) : -INFINITY;
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+// Loads of a tile: its base is uniform and a lane's place in it 32 bits, where pointers would take 64-bit
+// additions in the lanes, and registers for them.
+__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t more) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, at, more, 0);
+}
+__device__ __forceinline__ u32x2 load2(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t more) {
+    return __builtin_amdgcn_raw_buffer_load_b64(r, at, more, 0);
+}
+__device__ __forceinline__ u32x4 load4(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t more) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, at, more, 0);
+}
+
 // Parts go to the workspace and come back past the XCDs' own caches (agent scope: sc1), 16 bytes at a
 // time, which the language's atomics do not offer.
 constexpr int kAgent = 16;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t parts_of(float *p, int floats) {
-    return __builtin_amdgcn_make_buffer_rsrc(p, 0, floats * 4, 0x00020000);
-}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t parts_of(float *p, uint32_t floats) { return buffer_of(p, floats * 4); }
 __device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at * 4, 0, kAgent);
 }

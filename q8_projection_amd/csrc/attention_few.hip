@@ -7,6 +7,11 @@
 // head of several pieces is joined by the last workgroup to finish one, in the pieces' order.
 // Codes go from memory to registers, in the order of the matrix cores' operands, and become binary16
 // values there.
+//
+// v_mfma_f32_16x16x32_f16, as its lanes hold it (lane = 16 g + c):
+//   A: row c, depth 8 g + e (e = 0 .. 7);  B: column c, depth 8 g + e;  C: column c, rows 4 g + r
+// Scores: row c of half i is token 8 (c / 4) + 4 i + c % 4 of a tile, so that lane (g, c) gets row c's
+// scores of tokens 8 g + 4 i + r, i = 0, 1, and gives their weights to the sums.
 #include <algorithm>
 
 #include "attention.h"
@@ -30,6 +35,80 @@ struct FewArgs {
     int slot;           // floats of a part: rows * (D + 4)
 };
 
+// The largest, and the sum, over the four lanes of a column.
+__device__ __forceinline__ float column_max(float v) {
+    const float2 a = lane_pair32(v), b = lane_pair16(fmaxf(a.x, a.y));
+    return fmaxf(b.x, b.y);
+}
+__device__ __forceinline__ float column_sum(float v) {
+    const float2 a = lane_pair32(v), b = lane_pair16(a.x + a.y);
+    return b.x + b.y;
+}
+
+// The first dimension of the eight that step s of a score's product takes in lane group g; a lane's
+// codes lie together, up to 16 bytes.
+template <int BITS, int D>
+__device__ __forceinline__ constexpr int key_dims(int s, int g) {
+    if (BITS == 8) return 64 * (s / 2) + 16 * g + 8 * (s % 2);
+    return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s % 4);
+}
+
+// The dimensions of the output's products.  A lane's value codes come as kChunks 16-byte chunks of
+// the layout, kIn operands each.  Row c of operand (m, w) is dimension out_dim(c, m, w): with a
+// lane's chunks side by side, its dimensions lie in 2 (4 bits) or 1 blocks, and it needs the words of those alone.
+template <int BITS, int D>
+struct Out {
+    static constexpr int kChunks = BITS == 4 ? D / 64 : D / 32;
+    static constexpr int kIn = BITS == 4 ? 4 : 2;
+    static constexpr int kBlocks = BITS == 4 ? 2 : 1;
+    static constexpr int kPer = 16 / kChunks;  // rows of one unit of the layout
+    static constexpr int kUnit = BITS == 4 ? 64 : 32;  // dimensions of it
+
+    static __device__ __forceinline__ int unit(int c) { return c / kPer; }
+    static __device__ __forceinline__ int chunk(int c, int m) { return c % kPer * kChunks + m; }
+    static __device__ __forceinline__ int out_dim(int c, int m, int w) { return unit(c) * kUnit + 16 * w + chunk(c, m); }
+
+    // fn(first dimension, four values) for lane group g's part of a row's sums.
+    template <typename Acc, typename Fn>
+    static __device__ __forceinline__ void for_each_vec(Acc acc, int g, Fn fn) {
+#pragma unroll
+        for (int w = 0; w < kIn; ++w) {
+            if constexpr (kChunks == 1) {
+                fn(out_dim(4 * g, 0, w), acc(0, w));
+            } else if constexpr (kChunks == 2) {
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                    fn(out_dim(4 * g + r, 0, w), f32x4{acc(0, w)[r], acc(1, w)[r], acc(0, w)[r + 1], acc(1, w)[r + 1]});
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int m = 0; m < kChunks; m += 4)
+                        fn(out_dim(4 * g + r, m, w), f32x4{acc(m, w)[r], acc(m + 1, w)[r], acc(m + 2, w)[r], acc(m + 3, w)[r]});
+            }
+        }
+    }
+};
+
+// Scores of 32 tokens: lane (g, c) has row c's of tokens 8 g + 4 i + r in s[i][r].  Those that the row does
+// not see (outside [begin, end), t0 the first token) become -inf.
+__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int t0, int g, int begin, int end) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = t0 + 8 * g + 4 * i + r;
+            s[i][r] = t >= begin && t < end ? s[i][r] : -INFINITY;
+        }
+}
+
+__device__ __forceinline__ float largest(const f32x4 (&s)[2]) {
+    float most = s[0][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) most = fmaxf(most, s[e >> 2][e & 3]);
+    return most;
+}
+
 // Codes and words of a lane's keys, and of its values.
 template <int BITS, int D>
 struct Keys {
@@ -38,9 +117,8 @@ struct Keys {
     u32x4 x[2][kUnits];                                                  // (4 bits, D 64: half of it)
     uint32_t w[kUnits];
 
-    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t g, uint32_t c) {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t tile, uint32_t g, uint32_t c) {
         using T = Tile<BITS, D>;
-        // (unsigned offsets from a uniform pointer: no 64-bit arithmetic in the lanes)
         const uint32_t t = (c >> 2) * 8 + (c & 3);  // token of half 0
         const uint32_t code = t * T::kRow + g * (BITS == 4 && D == 64 ? 8 : 16);
         const uint32_t word = T::kKeyWords + (c * T::kBlocks + (BITS == 4 && D > 64 ? g : g >> 1)) * 4;
@@ -48,15 +126,15 @@ struct Keys {
         for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint8_t *p = tile + 4 * i * T::kRow + u * 64;
+                const uint32_t more = 4 * i * T::kRow + u * 64;
                 if (BITS == 4 && D == 64) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(p + code);
+                    const u32x2 v = load2(tile, code, more);
                     x[i][u] = u32x4{v.x, v.y, 0, 0};
                 } else {
-                    x[i][u] = *reinterpret_cast<const u32x4 *>(p + code);
+                    x[i][u] = load4(tile, code, more);
                 }
             }
-            w[u] = *reinterpret_cast<const uint32_t *>(tile + u * (BITS == 4 ? 16 : 8) + word);
+            w[u] = load1(tile, word, u * (BITS == 4 ? 16 : 8));
         }
     }
 };
@@ -66,15 +144,15 @@ struct Values {
     using O = Out<BITS, D>;
     u32x4 x[O::kChunks], w[O::kBlocks];
 
-    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t g, uint32_t c) {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t tile, uint32_t g, uint32_t c) {
         using T = Tile<BITS, D>;
         const uint32_t u = O::unit(c);
         const uint32_t code = T::kValues + ((u * 4 + g) * 16 + O::chunk(c, 0)) * 16;
         const uint32_t word = T::kValueWords + (u * O::kBlocks * 4 + g) * 16;
 #pragma unroll
-        for (int m = 0; m < O::kChunks; ++m) x[m] = *reinterpret_cast<const u32x4 *>(tile + m * 16 + code);
+        for (int m = 0; m < O::kChunks; ++m) x[m] = load4(tile, code, m * 16);
 #pragma unroll
-        for (int b = 0; b < O::kBlocks; ++b) w[b] = *reinterpret_cast<const u32x4 *>(tile + b * 64 + word);
+        for (int b = 0; b < O::kBlocks; ++b) w[b] = load4(tile, word, b * 64);
     }
 };
 
@@ -265,16 +343,17 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
             if (lane < mine && t * kTileTokens < hi) page = c.table[piece.s * c.table_ld + (t >> shift)];
             if (page < 0 || page >= c.pages) page = -1;
         };
-        const auto tile_of = [&](int l) -> const uint8_t * {
+        const auto tile_of = [&](int l) {
             const int t = span.first + base + l * WAVES;
             const int64_t pg = max(__builtin_amdgcn_readlane(page, l), 0);  // (none: the pool's first, not looked at)
-            return c.data + (((pg * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes;
+            return buffer_of(c.data + (((pg * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes,
+                             Tile<BITS, D>::kBytes);
         };
         Keys<BITS, D> keys;
         Values<BITS, D> values;
         look_up();
         if (mine) {
-            const uint8_t *tile = tile_of(0);
+            const __amdgpu_buffer_rsrc_t tile = tile_of(0);
             keys.load(tile, g, col);
             values.load(tile, g, col);
         }
@@ -296,7 +375,8 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                     row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
                 }
                 half8 *words = query + n * (D / 32) * 128 + lane;
-                const float t = load_query<BITS, D>(row, a.scale, g, [&](int s, half8 hi, half8 lo) {
+                const auto dims = [&](int s) { return key_dims<BITS, D>(s, g); };
+                const float t = load_query<BITS, D / 32>(row, a.scale, dims, column_max, [&](int s, half8 hi, half8 lo) {
                     words[2 * s * 64] = hi, words[(2 * s + 1) * 64] = lo;
                 });
                 if (g == 0) to_scores[x] = t;
@@ -317,7 +397,7 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                 const int t0 = (span.first + base + l * WAVES) * kTileTokens;
                 const Seen seen = {t0 < all_lo || t0 + kTileTokens > all_hi, t0, lo, hi};
                 const bool there = __builtin_amdgcn_readlane(page, l) >= 0;
-                const uint8_t *next = tile_of(min(l + 1, mine - 1));
+                const __amdgpu_buffer_rsrc_t next = tile_of(min(l + 1, mine - 1));
                 f32x4 z[NR][2];
                 if (there) w.scores(keys, query, lane, z);
                 keys.load(next, g, col);
@@ -325,8 +405,17 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         if (seen.masked) mask_scores(z[n], t0, g, max(w.begin[n], lo), min(w.end[n], hi));
-                        follow_max<O>(largest(z[n]) * w.to_score[n], w.top[n], w.sum[n], [&](int m, int j) -> f32x4 & { return w.acc[n][m][j]; });
-                        weights_of(z[n], w.to_score[n], w.top[n], w.sum[n], w.p_hi[n], w.p_lo[n]);
+                        follow_max(largest(z[n]) * w.to_score[n], w.top[n], w.sum[n], column_max, [&](float keep) {
+#pragma unroll
+                            for (int m = 0; m < O::kChunks; ++m)
+#pragma unroll
+                                for (int j = 0; j < O::kIn; ++j) w.acc[n][m][j] *= keep;
+                        });
+                        half2 p[4], q[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) weigh_pair(z[n][0][e], z[n][1][e], w.to_score[n], w.top[n], w.sum[n], p[e], q[e]);
+                        w.p_hi[n] = join(p[0], p[1], p[2], p[3]);
+                        w.p_lo[n] = join(q[0], q[1], q[2], q[3]);
                     }
                     w.add_values(values, seen, g);
                 }
@@ -335,7 +424,7 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
             base += 64 * WAVES;
             look_up();
             if (mine) {
-                const uint8_t *tile = tile_of(0);
+                const __amdgpu_buffer_rsrc_t tile = tile_of(0);
                 keys.load(tile, g, col);
                 values.load(tile, g, col);
             }

@@ -1,19 +1,29 @@
 // attention_rows.hip -- attention of many rows a sequence and kv head (prompts, chunks of prompts, drafts
 // of large groups): bound by the matrix cores.
 //
-// A workgroup of 4 waves takes a tile of 64 NR query rows of one sequence and kv head (a token's query heads
-// side by side), 16 NR a wave, and walks over the tiles of 32 tokens that they see.  Keys and values become
-// binary16 once for the workgroup: each wave turns a quarter of a tile's codes into operands of the matrix cores
-// and leaves them in LDS in the order in which a wave takes them (no bank conflicts).  A stage makes
-//   the weights of tile t from its scores,  the scores of tile t + 1,  the sums of tile t,
-//   the operands of tile t + 2's keys and t + 1's values,
+// A workgroup takes a tile of 128 query rows of one sequence and kv head (a token's query heads side by
+// side).  Four waves, with 32 rows each, walk over the tiles of 32 tokens that the rows see; four more over
+// every second of them, with the same rows, and their sums meet in LDS (256 dimensions: four waves alone, for the
+// registers).  So a SIMD has two waves, one's softmax beside the other's products, and a row tile is done in half the
+// time, which is what evens out causal prompts.  Keys and values become binary16 once for four waves: each
+// turns a quarter of a tile's codes into operands of the matrix cores and leaves them in LDS in the order in
+// which a wave takes them (no bank conflicts).  A stage makes
+//   the weights of tile t from its scores,  the scores of the tile after it,  the sums of tile t,
+//   the operands of the keys two tiles on and the values one tile on,
 // so that the softmax's and the conversion's instructions have products beside them that do not wait for
-// them; keys and values have two buffers each and one barrier a stage.
+// them; keys and values have two buffers each and one barrier a stage.  The 32 x 32 x 16 products leave
+// more room for other instructions beside them than the 16 x 16 x 32 ones, which take twice as many
+// operands from the registers for the same work.
 //
-// With as many row tiles as the chip holds workgroups, each is taken whole: the longest first, and every second round
-// over the CUs in the other order, so that what one CU gets of a causal prompt is about even.  Fewer stand in
-// one line, row tile after row tile, of which every workgroup takes an equal part; a row tile that
-// several share is joined by the last of them, in the order of the workgroups.
+// Many row tiles are taken whole, a prompt's last ones, which see most, first.  Fewer than two for each
+// workgroup that the chip holds stand in one line, sequence after sequence, of which every workgroup
+// takes an equal part; a row tile that several share is joined by the last of them, in the order of the workgroups.
+//
+// v_mfma_f32_32x32x16_f16, as its lanes hold it (lane = 32 h + c):
+//   A: row c, depth 8 h + e (e = 0 .. 7);  B: column c, depth 8 h + e;
+//   C: column c, rows 8 a + 4 h + j in register 4 a + j
+// Scores: row 8 a + 4 h + j is token 16 (a / 2) + 8 h + 4 (a % 2) + j of a tile, so that a lane gets row
+// c's scores of eight tokens in a row of each half of the tile, and gives their weights to the sums.
 #include <algorithm>
 
 #include "attention.h"
@@ -22,178 +32,207 @@
 namespace q8 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kPerCu = 2;
+constexpr int kTile = 128;     // query rows of a workgroup
 constexpr int kMinTiles = 16;  // tiles of a workgroup's part of the line, at least
 
-// Operands of 16 rows of a wave.
-template <int D>
-constexpr int kRowTiles = D == 256 ? 1 : 2;
+// Groups of four waves: 256 dimensions take twice the registers for queries and sums.
+constexpr int groups_of(int d) { return d == 256 ? 1 : 2; }
 
 struct RowsArgs {
     AttentionArgs a;
-    int cus;
-    int workgroups;
+    int workgroups;     // that the chip holds
     uint32_t *arrived;  // [workgroups], zero between calls
     float *parts;       // [2 workgroups][slot]
 };
 
 // Floats of a part: sums of a row tile, then (maximum, sum) of its rows.
-constexpr int slot_of(int d) { return (d == 256 ? 64 : 128) * (d + 4); }
+constexpr int slot_of(int d) { return kTile * (d + 4); }
 
 // The rows of tile `x` of a sequence's rows.
-__device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows &r, int x, int tile_rows) {
-    const int64_t from = int64_t(x) * tile_rows / a.group;
-    const int64_t to = min((int64_t(x) + 1) * tile_rows + a.group - 1, int64_t(r.n) * a.group) / a.group;
+__device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows &r, int x) {
+    const int64_t from = int64_t(x) * kTile / a.group;
+    const int64_t to = min((int64_t(x) + 1) * kTile + a.group - 1, int64_t(r.n) * a.group) / a.group;
     return {static_cast<int>(r.first + from), static_cast<int>(to - from), static_cast<int>(r.at + from), r.end};
 }
 
-// The line of row tiles: sequence after sequence, its last row tile first, kv heads side by side.  A row tile
-// is as long as its sequence's last one, the longest; or each is 1 long.
-template <int TILE>
+// The line of row tiles, sequence after sequence: with `whole` each is 1 long, the last one first and kv heads side
+// by side; else a kv head's row tiles follow one another, each about as long as the tiles of tokens that
+// it sees, which grow evenly from the sequence's first row tile to its last (fewer than kMaxLine row tiles).
+constexpr int kMaxLine = 1 << 16;
 struct Line {
-    int s0 = 0;  // sequences s0 .. s0 + 63 are the lanes'
+    bool whole;
+    int s0 = 0;          // sequences s0 .. s0 + 63 are the lanes'
     int64_t before = 0;  // the line's place of the first of them
     Rows rows;
-    int tiles, length;
+    int tiles, first, last;  // row tiles, and how much the first and the last see
     int64_t scan;
 
-    __device__ __forceinline__ void look(const AttentionArgs &a, int lane, bool whole) {
+    // Place of a kv head's row tile x.
+    static __device__ __forceinline__ int64_t place(int x, int tiles, int first, int last) {
+        const int64_t more = max(last - first, 0);
+        return int64_t(x) * first + (tiles > 1 ? more * x * (x - 1) / (2 * (tiles - 1)) : 0);
+    }
+    __device__ __forceinline__ void look(const AttentionArgs &a, int lane) {
         const int s = s0 + lane;
         rows = Rows{0, 0, 0, 0};
         if (s < a.c.sequences) rows = sequence_rows(a.c, s);
-        tiles = static_cast<int>((int64_t(rows.n) * a.group + TILE - 1) / TILE);
-        length = tiles ? (whole ? 1 : span_of(a, rows_of_tile(a, rows, tiles - 1, TILE)).n) : 0;
-        scan = wave_scan(int64_t(tiles) * length * a.c.kv_heads, lane);
+        tiles = static_cast<int>((int64_t(rows.n) * a.group + kTile - 1) / kTile);
+        first = last = 0;
+        if (tiles) first = span_of(a, rows_of_tile(a, rows, 0)).n, last = span_of(a, rows_of_tile(a, rows, tiles - 1)).n;
+        scan = wave_scan(a.c.kv_heads * (whole ? int64_t(tiles) : place(tiles, tiles, first, last)), lane);
     }
-    // All of it.
-    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int lane, bool whole) {
+    // All of it; then at the first sequences again.
+    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int lane) {
         int64_t all = 0;
         for (s0 = 0; s0 < a.c.sequences; s0 += 64) {
-            look(a, lane, whole);
+            look(a, lane);
             all += lane_of(scan, 63);
         }
-        begin(a, lane, whole);
+        s0 = 0;
+        if (a.c.sequences > 64) look(a, lane);
         return all;
     }
-    __device__ __forceinline__ void begin(const AttentionArgs &a, int lane, bool whole) {
-        before = 0;
-        if (s0 == 64 || s0 == 0) {  // (one round: the lanes have it)
-            const bool again = a.c.sequences > 64;
-            s0 = 0;
-            if (again) look(a, lane, whole);
-        } else {
-            s0 = 0;
-            look(a, lane, whole);
-        }
-    }
-    // The row tile at `at`, which is on the line.
+    // The row tile at `at`, which is on the line and not before the last one found.
     struct Item {
-        int s, tile, head, length;
-        int64_t origin;  // its place
+        int s, tile, head;
+        int64_t origin, length;
         Rows rows;
     };
-    __device__ __forceinline__ Item find(const AttentionArgs &a, int64_t at, int lane, bool whole) {
-        if (at < before) begin(a, lane, whole);
+    __device__ __forceinline__ Item find(const AttentionArgs &a, int64_t at, int lane) {
         uint64_t above;
         while (!(above = __ballot(before + scan > at)) && s0 + 64 < a.c.sequences) {
             before += lane_of(scan, 63);
             s0 += 64;
-            look(a, lane, whole);
+            look(a, lane);
         }
         const int l = above ? __builtin_ctzll(above) : 63;
+        const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+        const int64_t begin = before + (l ? lane_of(scan, l - 1) : 0);
+        const int n = of(tiles);
         Item it;
         it.s = s0 + l;
-        it.length = __builtin_amdgcn_readlane(length, l);
-        const int64_t place = before + (l ? lane_of(scan, l - 1) : 0);
-        const int64_t item = (at - place) / it.length;
-        it.origin = place + item * it.length;
-        it.head = static_cast<int>(item % a.c.kv_heads);
-        it.tile = __builtin_amdgcn_readlane(tiles, l) - 1 - static_cast<int>(item / a.c.kv_heads);
-        it.rows = Rows{__builtin_amdgcn_readlane(rows.first, l), __builtin_amdgcn_readlane(rows.n, l),
-                       __builtin_amdgcn_readlane(rows.at, l), __builtin_amdgcn_readlane(rows.end, l)};
+        it.rows = Rows{of(rows.first), of(rows.n), of(rows.at), of(rows.end)};
+        if (whole) {
+            const int64_t item = at - begin, x = item / a.c.kv_heads;
+            it.head = static_cast<int>(item - x * a.c.kv_heads);
+            it.tile = n - 1 - static_cast<int>(x);
+            it.origin = at;
+            it.length = 1;
+            return it;
+        }
+        const int f = of(first), e = of(last);
+        const int64_t head_length = place(n, n, f, e);
+        it.head = static_cast<int>((at - begin) / head_length);
+        const int64_t head_begin = begin + it.head * head_length, rest = at - head_begin;
+        for (int x0 = 0;; x0 += 64) {  // the last row tile whose place is not past `rest`
+            const uint64_t past = __ballot(x0 + lane + 1 >= n || place(x0 + lane + 1, n, f, e) > rest);
+            if (past) {
+                it.tile = x0 + __builtin_ctzll(past);
+                break;
+            }
+        }
+        const int64_t p = place(it.tile, n, f, e);
+        it.origin = head_begin + p;
+        it.length = place(it.tile + 1, n, f, e) - p;
         return it;
     }
 };
 
-// What a wave turns into operands of a tile: a quarter of the keys' codes, and of the values'.  Wave w takes half
-// w % 2 of the dimensions of the keys' 16 tokens w / 2, and D / 64 of the values' D / 16 operands.
+// What a wave turns into operands of a tile: a quarter of the keys' codes, and of the values'.  An operand of the
+// scores is 16 dimensions of the tile's tokens: step s has dimensions D / 2 h + 8 s + e; wave w makes steps
+// kMine w + ..
 template <int BITS, int D>
 struct KeyCodes {
     using T = Tile<BITS, D>;
-    static constexpr int kOperands = D / 64;
-    static constexpr int kDwords = kOperands * BITS / 4;      // a lane
-    static constexpr int kWords = BITS == 8 && D == 256 ? 2 : 1;
-    uint32_t x[kDwords], w[kWords];
+    static constexpr int kMine = D / 64;
+    static constexpr int kDwords = kMine * BITS / 4;  // a lane
+    uint32_t x[kDwords], w;
 
-    __device__ __forceinline__ void load(const uint8_t *tile, int wid, uint32_t g, uint32_t c) {
-        const uint32_t t = (c >> 2) * 8 + (c & 3), h = wid & 1;
-        const uint8_t *p = tile + 4 * (wid >> 1) * T::kRow;
-        // 16 bytes of a lane lie together: a quarter, a half or all of them, or two of them
-        constexpr bool kApart = BITS == 4 ? D == 256 : D >= 128;  // halves of the dimensions lie apart
-        const uint32_t at = t * T::kRow + (BITS == 4 && D == 64 ? g * 8 : g * 16) + h * (kApart ? D * BITS / 16 : 4 * kDwords);
+    // where a lane's codes and word are, and which half of the word's pair is its token's
+    struct Place {
+        uint32_t code, word, half;
+    };
+    static __device__ __forceinline__ Place place(uint32_t wid, uint32_t h, uint32_t c) {
+        const uint32_t t = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);  // row c's token
+        const uint32_t block = (h * (D / 2) + wid * 8 * kMine) / 32;
+        return {t * T::kRow + h * (T::kRow / 2) + wid * (4 * kDwords),
+                T::kKeyWords + 2 * (key_word(t, block, T::kBlocks) & ~1u), (c >> 3) & 1 ? 0x03020302u : 0x01000100u};
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t tile, const Place &p) {
         if constexpr (kDwords == 1) {
-            x[0] = *reinterpret_cast<const uint32_t *>(p + at);
+            x[0] = load1(tile, p.code, 0);
         } else if constexpr (kDwords == 2) {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(p + at);
+            const u32x2 v = load2(tile, p.code, 0);
             x[0] = v.x, x[1] = v.y;
         } else {
 #pragma unroll
             for (int u = 0; u < kDwords / 4; ++u) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(p + u * 64 + at);
+                const u32x4 v = load4(tile, p.code, u * 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[4 * u + e] = v[e];
             }
         }
-        const uint32_t block = (BITS == 4 && D > 64 ? g : g >> 1) + (kApart ? h * (D / 64) : 0);
-#pragma unroll
-        for (int u = 0; u < kWords; ++u)
-            w[u] = *reinterpret_cast<const uint32_t *>(tile + u * 8 + T::kKeyWords + (c * T::kBlocks + block) * 4);
+        w = load1(tile, p.word, 0);
     }
-    // operand e to [half][step][lane]
-    __device__ __forceinline__ void store(half8 *keys, int e, int wid, int lane) const {
+    // operand e to [step][lane]
+    __device__ __forceinline__ void store(half8 *keys, int e, int wid, int lane, const Place &p) const {
         Scales<BITS> s;
-        s.set(__builtin_amdgcn_perm(w[e * kWords / kOperands], w[e * kWords / kOperands], wid >> 1 ? 0x03020302u : 0x01000100u));
+        s.set(__builtin_amdgcn_perm(w, w, p.half));
         half8 v;
         if constexpr (BITS == 4) v = values_of(x[e], s, s, s, s);
         else v = values_of(x[2 * e], x[2 * e + 1], s, s, s, s);
-        keys[((wid >> 1) * (D / 32) + (wid & 1) * kOperands + e) * 64 + lane] = v;
+        keys[(wid * kMine + e) * 64 + lane] = v;
     }
 };
 
+// An operand (u, d) of the sums is 32 dimensions of tokens 16 u + 8 h + e; its row c is dimension
+// out_dim(c, d).  Wave w makes operands (w / 2, kMine (w % 2) + ..).
 template <int BITS, int D>
 struct ValueCodes {
     using T = Tile<BITS, D>;
-    using O = Out<BITS, D>;
-    static constexpr int kOperands = D / 64;
-    static constexpr int kDwords = kOperands * BITS / 4;
-    static constexpr int kBlocks = BITS == 4 && D == 256 ? 2 : 1;
+    static constexpr int kMine = D / 64;
+    static constexpr int kDwords = kMine * BITS / 4;
+    static constexpr int kBlocks = BITS == 4 && D == 256 ? 2 : BITS == 8 && D == 256 ? 2 : 1;
+    // A unit of the layout is 64 (4 bits) or 32 dimensions: 16 chunks of kIn times 16.  The rows' halves are
+    // units side by side, or (one unit) dimensions of one.
+    static constexpr int kUnit = BITS == 4 ? 64 : 32, kIn = kUnit / 16;
+    static constexpr bool kOneUnit = D == kUnit;
     uint32_t x[kDwords];
     u32x4 w[kBlocks];
 
-    __device__ __forceinline__ void load(const uint8_t *tile, int wid, uint32_t g, uint32_t c) {
-        // the wave's first operand is number wid * kOperands: (chunk, operand of it)
-        const uint32_t first = wid * kOperands, m = first / O::kIn, in = first % O::kIn, u = O::unit(c);
-        const uint32_t at = T::kValues + ((u * 4 + g) * 16 + O::chunk(c, 0) + m) * 16 + in * (BITS == 4 ? 4 : 8);
+    static __device__ __forceinline__ constexpr int out_dim(int c, int d) {
+        if (kOneUnit) return 32 * d + c;
+        return kUnit * (2 * (d / kIn) + c / 16) + 16 * (d % kIn) + c % 16;
+    }
+    struct Place {
+        uint32_t code, word;
+    };
+    static __device__ __forceinline__ Place place(uint32_t wid, uint32_t h, uint32_t c) {
+        const uint32_t a = 2 * (wid >> 1) + h, d = kMine * (wid & 1);
+        const uint32_t unit = kOneUnit ? 0 : 2 * (d / kIn) + (c >> 4), in = kOneUnit ? 2 * d + (c >> 4) : d % kIn;
+        // blocks of 32 dimensions: two a unit of 4 bits, one of 8
+        const uint32_t block = BITS == 4 ? 2 * unit + in / 2 : unit;
+        return {T::kValues + ((unit * 4 + a) * 16 + (c & 15)) * 16 + in * (BITS == 4 ? 4 : 8), T::kValueWords + (block * 4 + a) * 16};
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t tile, const Place &p) {
         if constexpr (kDwords == 1) {
-            x[0] = *reinterpret_cast<const uint32_t *>(tile + at);
+            x[0] = load1(tile, p.code, 0);
         } else if constexpr (kDwords == 2) {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(tile + at);
+            const u32x2 v = load2(tile, p.code, 0);
             x[0] = v.x, x[1] = v.y;
-        } else {
+        } else {  // 16 bytes of a unit; a wave's second ones lie two units on
 #pragma unroll
             for (int q = 0; q < kDwords / 4; ++q) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(tile + 16 * q + at);
+                const u32x4 v = load4(tile, p.code, q * (2 * 4 * 16 * 16));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
             }
         }
-        const uint32_t block = BITS == 4 ? 2 * u + (kBlocks == 1 ? in / 2 : 0) : u;
+        constexpr uint32_t kNext = BITS == 4 ? 1 : 2;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) w[b] = *reinterpret_cast<const u32x4 *>(tile + b * 64 + T::kValueWords + (block * 4 + g) * 16);
+        for (int b = 0; b < kBlocks; ++b) w[b] = load4(tile, p.word, b * kNext * 64);
     }
-    // operand e to [operand][lane]
+    // operand e to [u][d][lane]
     __device__ __forceinline__ void store(half8 *values, int e, int wid, int lane) const {
         Scales<BITS> s[4];
 #pragma unroll
@@ -201,44 +240,63 @@ struct ValueCodes {
         half8 v;
         if constexpr (BITS == 4) v = values_of(x[e], s[0], s[1], s[2], s[3]);
         else v = values_of(x[2 * e], x[2 * e + 1], s[0], s[1], s[2], s[3]);
-        values[(wid * kOperands + e) * 64 + lane] = v;
+        values[((wid >> 1) * (D / 32) + (wid & 1) * kMine + e) * 64 + lane] = v;
     }
 };
 
+__device__ __forceinline__ float column_max(float v) {
+    const float2 a = lane_pair32(v);
+    return fmaxf(a.x, a.y);
+}
+__device__ __forceinline__ float column_sum(float v) {
+    const float2 a = lane_pair32(v);
+    return a.x + a.y;
+}
+
+__device__ __forceinline__ float largest(const f32x16 &z) {
+    float most = z[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) most = fmaxf(most, z[e]);
+    return most;
+}
+
 template <int BITS, int D>
-__global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
-    using O = Out<BITS, D>;
-    constexpr int NR = kRowTiles<D>, kTile = 64 * NR, kSteps = D / 32, kSlot = slot_of(D);
-    __shared__ half8 keys[2][2 * kSteps * 64], values[2][D / 16 * 64];
+__global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(RowsArgs f) {
+    using V = ValueCodes<BITS, D>;
+    constexpr int kSteps = D / 16, kDims = D / 32, kMine = D / 64, kSlot = slot_of(D);
+    constexpr int kGroups = groups_of(D), kThreads = 256 * kGroups;
+    // A group's operands: keys, keys of the next tile, values, values of the next tile.  As large as the sums of
+    // a group's waves, which meet there.
+    constexpr int kKeys = kSteps * 64, kValues = 2 * kDims * 64, kOperands = 2 * (kKeys + kValues);
+    static_assert(kOperands * kGroups * 16 >= (kGroups - 1) * kTile * D * 4);
+    __shared__ half8 operands[kGroups][kOperands];
+    __shared__ float tops[256], sums[256];
     __shared__ uint32_t last;
     const AttentionArgs &a = f.a;
     const CacheArgs &c = a.c;
-    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
-    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave & 3, group = wave >> 2;
+    half8 *const keys = operands[group], *const values = keys + 2 * kKeys;
 
-    Line<kTile> line;
-    int64_t all = line.measure(a, lane, true);
-    const bool whole = all >= f.workgroups;
+    Line line;
+    line.whole = true;
+    int64_t all = line.measure(a, lane);
+    line.whole = all >= 2 * int64_t(f.workgroups) || all >= kMaxLine;
     int64_t chunk = 1;
-    if (!whole) {
-        line.s0 = 0;
-        all = line.measure(a, lane, false);
+    if (!line.whole) {
+        all = line.measure(a, lane);
         chunk = max((all + f.workgroups - 1) / f.workgroups, int64_t(kMinTiles));
     }
 
     for (int64_t p = blockIdx.x; p * chunk < all; p += gridDim.x) {
-        int64_t at = p * chunk, stop = min(at + chunk, all);
-        if (whole) {  // every second round over the CUs backwards
-            const int64_t round = p / f.cus, size = min(int64_t(f.cus), all - round * f.cus);
-            if (round & 1) at = round * f.cus + size - 1 - (p - round * f.cus);
-            stop = at + 1;
-        }
+        int64_t at = p * chunk;
+        const int64_t stop = min(at + chunk, all);
         while (at < stop) {
-            const typename Line<kTile>::Item it = line.find(a, at, lane, whole);
-            const Rows r = it.rows, tile_rows = rows_of_tile(a, r, it.tile, kTile);
+            const Line::Item it = line.find(a, at, lane);
+            const Rows r = it.rows, tile_rows = rows_of_tile(a, r, it.tile);
             const Span span = span_of(a, tile_rows);
             // this workgroup's share of the row tile
-            const int64_t share_end = min(stop - it.origin, int64_t(it.length));
+            const int64_t share_end = min(stop - it.origin, it.length);
             const int from = static_cast<int>(int64_t(span.n) * (at - it.origin) / it.length);
             const int to = static_cast<int>(int64_t(span.n) * share_end / it.length);
             const bool alone = at == it.origin && share_end == it.length, begins = at == it.origin;
@@ -261,163 +319,169 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
                 if (page < 0 || page >= c.pages) page = -1;
             };
             const auto page_of = [&](int tile) { return __builtin_amdgcn_readlane(page, tile - paged); };
-            const auto tile_in = [&](int tile, int pg) -> const uint8_t * {  // (none: the pool's first, not looked at)
+            const auto tile_in = [&](int tile, int pg) {  // (none: the pool's first, not looked at)
                 const int t = span.first + tile;
-                return c.data + (((int64_t(max(pg, 0)) * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes;
+                return buffer_of(c.data + (((int64_t(max(pg, 0)) * c.kv_heads + head) << shift) + (t & ((1 << shift) - 1))) * Tile<BITS, D>::kBytes, Tile<BITS, D>::kBytes);
             };
 
             KeyCodes<BITS, D> kc;
-            ValueCodes<BITS, D> vc;
+            V vc;
+            const auto kp = KeyCodes<BITS, D>::place(wid, h, col);
+            const auto vp = V::place(wid, h, col);
             // the value words of tokens that are not there are no value's
             const auto clear_words = [&](int tile, int pg) {
                 const int t0 = (span.first + tile) * kTileTokens;
                 if (pg >= 0 && t0 >= lo && t0 + kTileTokens <= hi) return;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int t = t0 + 8 * g + q;
+                    const int t = t0 + 16 * (wid >> 1) + 8 * h + q;
                     const uint32_t there = (t >= lo && t < hi ? 0xffffu : 0u) | (t + 4 >= lo && t + 4 < hi ? 0xffff0000u : 0u);
 #pragma unroll
                     for (auto &w : vc.w) w[q] = pg < 0 ? 0u : w[q] & there;
                 }
             };
+            // a group's tiles: begin, begin + kGroups, ..; the pages of the next two
+            const int begin = from + group;
             look_up(from);
-            // pages of tile + 1, tile + 2
-            int page1 = page_of(from + 1), page2 = page_of(from + 2);
-            const int page0 = page_of(from);
-            kc.load(tile_in(from, page0), wid, g, col);
-            vc.load(tile_in(from, page0), wid, g, col);
+            const int page0 = page_of(begin);
+            int page1 = page_of(begin + kGroups), page2 = page_of(begin + 2 * kGroups);
+            kc.load(tile_in(begin, page0), kp);
+            vc.load(tile_in(begin, page0), vp);
 
-            half8 q_hi[NR][kSteps], q_lo[NR][kSteps];
-            float to_score[NR], top[NR], sum[NR];
-            f32x4 acc[O::kChunks][O::kIn][NR];  // row operands last
-            const int first_row = row0 + wid * 16 * NR;
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const int x = first_row + n * 16 + col;
-                const float *row = nullptr;
-                if (x < rows) {
-                    const Where q = where(a, r, head, x);
-                    row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
-                }
-                to_score[n] = load_query<BITS, D>(row, a.scale, g, [&](int s, half8 h, half8 l) { q_hi[n][s] = h, q_lo[n][s] = l; });
-                top[n] = kNoMax;
-                sum[n] = 0.0f;
-#pragma unroll
-                for (int m = 0; m < O::kChunks; ++m)
-#pragma unroll
-                    for (int j = 0; j < O::kIn; ++j) acc[m][j][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            half8 q_hi[kSteps], q_lo[kSteps];
+            const int x = row0 + wid * 32 + col;  // the lane's row
+            const float *row = nullptr;
+            if (x < rows) {
+                const Where q = where(a, r, head, x);
+                row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
             }
+            const float to_score = load_query<BITS, kSteps>(row, a.scale, [&](int s) { return D / 2 * h + 8 * s; }, column_max,
+                                                            [&](int s, half8 hi8, half8 lo8) { q_hi[s] = hi8, q_lo[s] = lo8; });
+            float top = kNoMax, sum = 0.0f;
+            f32x16 acc[kDims];
+#pragma unroll
+            for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
 
-            const auto scores = [&](int tile, f32x4(&z)[NR][2]) {
-                const half8 *k = keys[tile & 1] + lane;
-#pragma unroll
-                for (int n = 0; n < NR; ++n) z[n][0] = z[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const half8 k0 = k[s * 64], k1 = k[(kSteps + s) * 64];
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) z[n][0] = mfma(k0, q_hi[n][s], z[n][0]), z[n][1] = mfma(k1, q_hi[n][s], z[n][1]);
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) z[n][0] = mfma(k0, q_lo[n][s], z[n][0]), z[n][1] = mfma(k1, q_lo[n][s], z[n][1]);
-                }
-            };
-            // What a row does not see of a tile, and the maximum.
-            const auto settle = [&](int tile, int pg, f32x4(&z)[NR][2], float (&most)[NR]) {
+            // What the row does not see of a tile, and the maximum.
+            const auto settle = [&](int tile, int pg, f32x16 &z, float most) {
                 const int t0 = (span.first + tile) * kTileTokens;
                 if (pg < 0 || t0 < all_lo || t0 + kTileTokens > all_hi) {
+                    const int t = r.at + x / a.group;
+                    const int from_token = a.window ? t - a.window + 1 : 0, end = pg < 0 || x >= rows ? 0 : min(t + 1, r.end);
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const int x = first_row + n * 16 + col, t = r.at + x / a.group;
-                        const int end = pg < 0 || x >= rows ? 0 : min(t + 1, r.end);
-                        mask_scores(z[n], t0, g, a.window ? t - a.window + 1 : 0, end);
-                        most[n] = largest(z[n]);
+                    for (int e = 0; e < 16; ++e) {
+                        const int token = t0 + 16 * (e >> 3) + 8 * h + (e & 7);
+                        z[e] = token >= from_token && token < end ? z[e] : -INFINITY;
                     }
+                    most = largest(z);
                 }
+                follow_max(most * to_score, top, sum, column_max, [&](float keep) {
 #pragma unroll
-                for (int n = 0; n < NR; ++n) follow_max<O>(most[n] * to_score[n], top[n], sum[n], [&](int m, int j) -> f32x4 & { return acc[m][j][n]; });
+                    for (int d = 0; d < kDims; ++d) acc[d] *= keep;
+                });
             };
 
             // keys of the first two tiles, values of the first
-            constexpr int kMine = D / 64;  // operands of keys, and of values, that a wave makes
-            clear_words(from, page0);
+            clear_words(begin, page0);
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) kc.store(keys[from & 1], e, wid, lane), vc.store(values[from & 1], e, wid, lane);
-            kc.load(tile_in(from + 1, page1), wid, g, col);
-            vc.load(tile_in(from + 1, page1), wid, g, col);
+            for (int e = 0; e < kMine; ++e) kc.store(keys, e, wid, lane, kp), vc.store(values, e, wid, lane);
+            kc.load(tile_in(begin + kGroups, page1), kp);
+            vc.load(tile_in(begin + kGroups, page1), vp);
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) kc.store(keys[(from + 1) & 1], e, wid, lane);
-            kc.load(tile_in(from + 2, page2), wid, g, col);
-            clear_words(from + 1, page1);
+            for (int e = 0; e < kMine; ++e) kc.store(keys + kKeys, e, wid, lane, kp);
+            kc.load(tile_in(begin + 2 * kGroups, page2), kp);
+            clear_words(begin + kGroups, page1);
             __syncthreads();
-            f32x4 z[NR][2];
-            float most[NR];
-            if (from < to) {
-                scores(from, z);
+            f32x16 z;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) most[n] = largest(z[n]);
-                settle(from, page0, z, most);
-            }
+            for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) z = mfma(keys[s * 64 + lane], q_hi[s], z), z = mfma(keys[s * 64 + lane], q_lo[s], z);
+            settle(begin, page0, z, largest(z));
             __syncthreads();
-            for (int tile = from; tile < to; ++tile) {
-                if (tile + 3 - paged > 63) look_up(tile);
-                const int page3 = page_of(tile + 3);
+            // Past the last tile a group's page is none: its weights there are zeros.
+            for (int tile = begin, odd = 0; tile - group < to; tile += kGroups, odd ^= 1) {
+                if (tile + 3 * kGroups - paged > 63) look_up(tile);
+                const int page3 = page_of(tile + 3 * kGroups);
                 // The weights of this tile beside the scores of the next.  The order of the steps is kept (the
                 // barriers), for the compiler makes all weights and then all products.
-                half2 p_hi[NR][4], p_lo[NR][4];
-                f32x4 next[NR][2];
+                half2 p_hi[2][4], p_lo[2][4];
+                f32x16 next;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) next[n][0] = next[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-                const half8 *k = keys[(tile + 1) & 1] + lane, *v = values[tile & 1] + lane;
-                half8 k0 = k[0], k1 = k[kSteps * 64], k0_next = k0, k1_next = k1;
-                half8 x = v[0], x_next = x;
+                for (int e = 0; e < 16; ++e) next[e] = 0.0f;
+                half8 *const now_keys = keys + (odd ? kKeys : 0), *const now_values = values + (odd ? kValues : 0);
+                const half8 *k = keys + (odd ? 0 : kKeys) + lane, *v = now_values + lane;
+                half8 *const next_values = values + (odd ? 0 : kValues);
+                half8 operand = k[0], after = operand;
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int s = 0; s < 2 * kSteps; ++s) {
-                    if (s % 2 == 0 && s / 2 + 1 < kSteps) k0_next = k[(s / 2 + 1) * 64], k1_next = k[(kSteps + s / 2 + 1) * 64];
+                for (int s = 0; s < kSteps; ++s) {
+                    after = s + 1 < kSteps ? k[(s + 1) * 64] : v[0];
+                    next = mfma(operand, q_hi[s], next);
+                    next = mfma(operand, q_lo[s], next);
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const half8 q = s % 2 ? q_lo[n][s / 2] : q_hi[n][s / 2];
-                        next[n][0] = mfma(k0, q, next[n][0]);
-                        next[n][1] = mfma(k1, q, next[n][1]);
+                    for (int i = s * 8 / kSteps; i < (s + 1) * 8 / kSteps; ++i) {
+                        const int u = i / 4, p = i % 4;
+                        weigh_pair(z[8 * u + p], z[8 * u + 4 + p], to_score, top, sum, p_hi[u][p], p_lo[u][p]);
                     }
-#pragma unroll
-                    for (int i = s * 4 * NR / (2 * kSteps); i < (s + 1) * 4 * NR / (2 * kSteps); ++i)
-                        weigh_pair(z[i / 4], i % 4, to_score[i / 4], top[i / 4], sum[i / 4], p_hi[i / 4][i % 4], p_lo[i / 4][i % 4]);
-                    if (s % 2) k0 = k0_next, k1 = k1_next;
+                    operand = after;
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                half8 w_hi[NR], w_lo[NR];
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    w_hi[n] = join(p_hi[n][0], p_hi[n][1], p_hi[n][2], p_hi[n][3]);
-                    w_lo[n] = join(p_lo[n][0], p_lo[n][1], p_lo[n][2], p_lo[n][3]);
-                    z[n][0] = next[n][0], z[n][1] = next[n][1];
-                }
+                z = next;
                 // The sums of this tile beside the next operands.
+                float most = kNoMax;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    if (j + 1 < D / 16) x_next = v[(j + 1) * 64];
-                    f32x4(&o)[NR] = acc[j / O::kIn][j % O::kIn];
+                for (int j = 0; j < 2 * kDims; ++j) {
+                    const int u = j / kDims, d = j % kDims;
+                    if (j + 1 < 2 * kDims) after = v[(j + 1) * 64];
+                    acc[d] = mfma(operand, join(p_hi[u][0], p_hi[u][1], p_hi[u][2], p_hi[u][3]), acc[d]);
+                    acc[d] = mfma(operand, join(p_lo[u][0], p_lo[u][1], p_lo[u][2], p_lo[u][3]), acc[d]);
+                    constexpr int kWork = 2 * kMine + 1;
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) o[n] = mfma(x, w_hi[n], o[n]);
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) o[n] = mfma(x, w_lo[n], o[n]);
-                    constexpr int kWork = 2 * kMine + NR;
-#pragma unroll
-                    for (int i = j * kWork / (D / 16); i < (j + 1) * kWork / (D / 16); ++i) {
-                        if (i < kMine) kc.store(keys[tile & 1], i, wid, lane);
-                        if (i == kMine - 1) kc.load(tile_in(tile + 3, page3), wid, g, col);
-                        if (i >= kMine && i < 2 * kMine) vc.store(values[(tile + 1) & 1], i - kMine, wid, lane);
-                        if (i == 2 * kMine - 1) vc.load(tile_in(tile + 2, page2), wid, g, col);
-                        if (i >= 2 * kMine) most[i - 2 * kMine] = largest(z[i - 2 * kMine]);
+                    for (int i = j * kWork / (2 * kDims); i < (j + 1) * kWork / (2 * kDims); ++i) {
+                        if (i < kMine) kc.store(now_keys, i, wid, lane, kp);
+                        if (i == kMine - 1) kc.load(tile_in(tile + 3 * kGroups, page3), kp);
+                        if (i >= kMine && i < 2 * kMine) vc.store(next_values, i - kMine, wid, lane);
+                        if (i == 2 * kMine - 1) vc.load(tile_in(tile + 2 * kGroups, page2), vp);
+                        if (i == 2 * kMine) most = largest(z);
                     }
-                    x = x_next;
+                    operand = after;
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (tile + 1 < to) settle(tile + 1, page1, z, most);
-                clear_words(tile + 2, page2);
+                settle(tile + kGroups, page1, z, most);
+                clear_words(tile + 2 * kGroups, page2);
                 page1 = page2, page2 = page3;
                 __syncthreads();
+            }
+
+            if constexpr (kGroups == 2) {  // the other group's sums, lane by lane
+                f32x4 *meet = reinterpret_cast<f32x4 *>(&operands[0][0]) + wid * (kDims * 4 * 64) + lane;
+                if (group == 1) {
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            meet[(d * 4 + e) * 64] = f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]};
+                    tops[wid * 64 + lane] = top;
+                    sums[wid * 64 + lane] = sum;
+                }
+                __syncthreads();
+                if (group == 0) {
+                    const float other = tops[wid * 64 + lane], now = fmaxf(top, other);
+                    const float keep = exp2_of(top - now), more = exp2_of(other - now);
+                    top = now;
+                    sum = sum * keep + sums[wid * 64 + lane] * more;
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const f32x4 o = meet[(d * 4 + e) * 64];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[d][4 * e + j] = acc[d][4 * e + j] * keep + o[j] * more;
+                        }
+                }
             }
 
             // A part: rows of D sums, then rows of (maximum, sum).  A workgroup has two at most: one that ends
@@ -425,20 +489,21 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
             const __amdgpu_buffer_rsrc_t parts = parts_of(f.parts, 2 * f.workgroups * kSlot);
             const auto part = [&](int i) { return static_cast<uint32_t>(2 * (first + i) + (i == 0)) * kSlot; };
             const uint32_t mine = (2 * static_cast<uint32_t>(p) + begins) * kSlot;
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const int x = first_row + n * 16 + col;
-                const float total = column_sum(sum[n]);
-                if (x >= rows) continue;
+            const float total = column_sum(sum);
+            if (x < rows && group == 0) {
                 constexpr float kScale = Scales<BITS>::kUp;
-                if (alone) {
-                    const Where to_row = where(a, r, head, x);
-                    O::for_each_vec([&](int m, int j) { return acc[m][j][n]; }, g, [&](int dim, f32x4 o) { write_row<D>(a, to_row, dim, o * kScale, total, top[n]); });
-                } else {
-                    const int y = x - row0;
-                    O::for_each_vec([&](int m, int j) { return acc[m][j][n]; }, g, [&](int dim, f32x4 o) { store_part(parts, mine + y * D + dim, o * kScale); });
-                    if (g == 0) store_part(parts, mine + kTile * D + 4 * y, f32x4{top[n], total, 0.f, 0.f});
-                }
+                const Where to_row = where(a, r, head, x);
+                const int y = x - row0;
+#pragma unroll
+                for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const f32x4 o = f32x4{acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]} * kScale;
+                        const int dim = V::out_dim(2 * e + 4 * h, d);
+                        if (alone) write_row<D>(a, to_row, dim, o, total, top);
+                        else store_part(parts, mine + y * D + dim, o);
+                    }
+                if (!alone && h == 0) store_part(parts, mine + kTile * D + 4 * y, f32x4{top, total, 0.f, 0.f});
             }
             if (!alone) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -478,16 +543,15 @@ __global__ __launch_bounds__(kThreads, kPerCu) void rows_kernel(RowsArgs f) {
     }
 }
 
-int rows_workgroups() { return device_info().cus * kPerCu; }
+int rows_workgroups() { return device_info().cus; }
 
 template <int BITS, int D>
 hipError_t run(const RowsArgs &f, hipStream_t stream) {
-    constexpr int kTile = 64 * kRowTiles<D>;
     // a workgroup for each row tile there may be, unless there are very many
     const int64_t row_tiles = (int64_t(f.a.c.max_rows) * f.a.group + kTile - 1) / kTile;
     const int64_t most = std::max<int64_t>(f.workgroups, f.a.c.sequences * f.a.c.kv_heads * row_tiles);
-    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(most, 16 * int64_t(f.workgroups))));
-    rows_kernel<BITS, D><<<grid, kThreads, 0, stream>>>(f);
+    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(most, 32 * int64_t(f.workgroups))));
+    rows_kernel<BITS, D><<<grid, 256 * groups_of(D), 0, stream>>>(f);
     return hipGetLastError();
 }
 
@@ -498,7 +562,6 @@ int64_t rows_workspace(int dim) { return attention_counter_bytes() + int64_t(2) 
 hipError_t launch_rows(int bits, int dim, const AttentionArgs &a, void *workspace, hipStream_t stream) {
     RowsArgs f = {};
     f.a = a;
-    f.cus = device_info().cus;
     f.workgroups = rows_workgroups();
     f.arrived = static_cast<uint32_t *>(workspace);
     f.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + attention_counter_bytes());
