@@ -197,15 +197,14 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
                                 static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)));
 }
 // Inclusive sum over the lanes.
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t up = __shfl_up(v, off, 64);
-        v += lane >= off ? up : 0;
-    }
-    return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t add_dpp(int64_t v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xf, false);
+    return v + static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo));
 }
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
     v = add_dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
     v = add_dpp<0x112, 0xf>(v);
     v = add_dpp<0x114, 0xf>(v);

@@ -45,8 +45,8 @@ struct RowsArgs {
     float *parts;       // [2 workgroups][slot]
 };
 
-// Floats of a part: sums of a row tile, then (maximum, sum) of its rows.
-constexpr int slot_of(int d) { return kTile * (d + 4); }
+// Floats of a part: a row tile's sums, and (maximum, sum, -, -) for each lane of four waves.
+constexpr int slot_of(int d) { return kTile * (d + 8); }
 
 // The rows of tile `x` of a sequence's rows.
 __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows &r, int x) {
@@ -79,7 +79,7 @@ struct Line {
         tiles = static_cast<int>((int64_t(rows.n) * a.group + kTile - 1) / kTile);
         first = last = 0;
         if (tiles) first = span_of(a, rows_of_tile(a, rows, 0)).n, last = span_of(a, rows_of_tile(a, rows, tiles - 1)).n;
-        scan = wave_scan(a.c.kv_heads * (whole ? int64_t(tiles) : place(tiles, tiles, first, last)), lane);
+        scan = wave_scan(a.c.kv_heads * (whole ? int64_t(tiles) : place(tiles, tiles, first, last)));
     }
     // All of it; then at the first sequences again.
     __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int lane) {
@@ -264,7 +264,7 @@ template <int BITS, int D>
 __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(RowsArgs f) {
     using V = ValueCodes<BITS, D>;
     constexpr int kSteps = D / 16, kDims = D / 32, kMine = D / 64, kSlot = slot_of(D);
-    constexpr int kGroups = groups_of(D), kThreads = 256 * kGroups;
+    constexpr int kGroups = groups_of(D);
     // A group's operands: keys, keys of the next tile, values, values of the next tile.  As large as the sums of
     // a group's waves, which meet there.
     constexpr int kKeys = kSteps * 64, kValues = 2 * kDims * 64, kOperands = 2 * (kKeys + kValues);
@@ -484,29 +484,25 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
                 }
             }
 
-            // A part: rows of D sums, then rows of (maximum, sum).  A workgroup has two at most: one that ends
-            // a row tile, and one that begins one, of which the second place is.
-            const __amdgpu_buffer_rsrc_t parts = parts_of(f.parts, 2 * f.workgroups * kSlot);
-            const auto part = [&](int i) { return static_cast<uint32_t>(2 * (first + i) + (i == 0)) * kSlot; };
-            const uint32_t mine = (2 * static_cast<uint32_t>(p) + begins) * kSlot;
-            const float total = column_sum(sum);
-            if (x < rows && group == 0) {
-                constexpr float kScale = Scales<BITS>::kUp;
-                const Where to_row = where(a, r, head, x);
-                const int y = x - row0;
-#pragma unroll
-                for (int d = 0; d < kDims; ++d)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const f32x4 o = f32x4{acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]} * kScale;
-                        const int dim = V::out_dim(2 * e + 4 * h, d);
-                        if (alone) write_row<D>(a, to_row, dim, o, total, top);
-                        else store_part(parts, mine + y * D + dim, o);
-                    }
-                if (!alone && h == 0) store_part(parts, mine + kTile * D + 4 * y, f32x4{top, total, 0.f, 0.f});
-            }
+            sum = column_sum(sum);
             if (!alone) {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                // A part: a wave's sums as its lanes hold them, then the rows' (maximum, sum), lane by lane.  A
+                // workgroup has two at most: one that ends a row tile, and one that begins one, of which the second
+                // place is.
+                const __amdgpu_buffer_rsrc_t parts = parts_of(f.parts, 2 * f.workgroups * kSlot);
+                const auto part = [&](int i, bool begins) {
+                    return static_cast<uint32_t>(2 * i + begins) * kSlot + wid * (kSlot / 4) + 4 * lane;
+                };
+                if (group == 0) {
+                    const uint32_t mine = part(static_cast<int>(p), begins);
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            store_part(parts, mine + (4 * d + e) * 256, f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]});
+                    store_part(parts, mine + kDims * 1024, f32x4{top, sum, 0.f, 0.f});
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                }
                 __syncthreads();
                 if (threadIdx.x == 0) {
                     uint32_t *counter = f.arrived + first;
@@ -515,28 +511,38 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
                     if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 }
                 __syncthreads();
-                if (last) {
-                    const int vecs = min(rows - row0, kTile) * (D / 4);
-                    for (int e = threadIdx.x; e < vecs; e += kThreads) {
-                        const int y = e / (D / 4), dim = e % (D / 4) * 4;
-                        Sums joined;
-                        constexpr int kAhead = 4;
-                        for (int i = 0; i < sharers; i += kAhead) {
-                            f32x4 o[kAhead], st[kAhead];
+                if (group == 0 && last) {  // all of them, in the workgroups' order
+                    top = kNoMax;
+                    sum = 0.0f;
 #pragma unroll
-                            for (int j = 0; j < kAhead; ++j) {
-                                // (past the last one: past the buffer, nothing is read)
-                                const uint32_t place = part(i + j) | oob_bit(i + j < sharers) >> 2;
-                                st[j] = load_part(parts, place + kTile * D + 4 * y);
-                                o[j] = load_part(parts, place + 4 * e);
-                            }
+                    for (int d = 0; d < kDims; ++d)
 #pragma unroll
-                            for (int j = 0; j < kAhead; ++j)
-                                if (i + j < sharers) joined.add(o[j], st[j].x, st[j].y);
-                        }
-                        write_row<D>(a, where(a, r, head, row0 + y), dim, joined.o, joined.sum, joined.top);
+                        for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
+                    for (int i = 0; i < sharers; ++i) {
+                        const uint32_t from_part = part(first + i, i == 0);
+                        const f32x4 st = load_part(parts, from_part + kDims * 1024);
+                        f32x4 o[kDims * 4];
+#pragma unroll
+                        for (int e = 0; e < kDims * 4; ++e) o[e] = load_part(parts, from_part + e * 256);
+                        const float now = fmaxf(top, st.x), keep = exp2_of(top - now), more = exp2_of(st.x - now);
+                        top = now;
+                        sum = sum * keep + st.y * more;
+#pragma unroll
+                        for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) acc[d][e] = acc[d][e] * keep + o[4 * d + e / 4][e % 4] * more;
                     }
                 }
+            }
+            if (x < rows && group == 0 && (alone || last)) {
+                constexpr float kScale = Scales<BITS>::kUp;
+                const Where to_row = where(a, r, head, x);
+#pragma unroll
+                for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        write_row<D>(a, to_row, V::out_dim(2 * e + 4 * h, d),
+                                     f32x4{acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]} * kScale, sum, top);
             }
             __syncthreads();  // LDS is free again
         }
