@@ -138,26 +138,38 @@ __device__ __forceinline__ uint32_t lift_of(float most) {
     return static_cast<uint32_t>(min(141 + 127 - e, 253)) << 23;
 }
 
-// A query row as B operands of the scores' products: q * scale * log2(e), lifted, out(step, hi, lo) for
-// each of STEPS.  The row is the lane's column's (null: none, zeros); dims(step) is the first of the eight
-// dimensions that the lane has of a step, column_max the largest over a column's lanes.  Returns what a
-// score is multiplied by: a power of two.
-template <int BITS, int STEPS, typename Dims, typename Max, typename Fn>
-__device__ __forceinline__ float load_query(const float *row, float scale, Dims dims, Max column_max, Fn out) {
+// A query row as B operands of the scores' products, eight dimensions from dims(step) on for a lane and step.
+template <int STEPS>
+struct QueryRow {
+    float x[STEPS][8];
+
+    // (null: zeros)
+    template <typename Dims>
+    __device__ __forceinline__ void load(const float *row, Dims dims) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (row) {
+                const float4 *p = reinterpret_cast<const float4 *>(row + dims(s));
+                a = p[0], b = p[1];
+            }
+            x[s][0] = a.x, x[s][1] = a.y, x[s][2] = a.z, x[s][3] = a.w, x[s][4] = b.x, x[s][5] = b.y, x[s][6] = b.z, x[s][7] = b.w;
+        }
+    }
+};
+
+// The row times scale * log2(e), lifted, as operands: out(step, hi, lo).  column_max is the largest over a
+// column's lanes.  Returns what a score is multiplied by: a power of two.
+template <int BITS, int STEPS, typename Max, typename Fn>
+__device__ __forceinline__ float query_words(const QueryRow<STEPS> &row, float scale, Max column_max, Fn out) {
     float x[STEPS][8];
     float most = 0.0f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (row) {
-            const float4 *p = reinterpret_cast<const float4 *>(row + dims(s));
-            a = p[0], b = p[1];
-        }
-        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             // the order of values_of: pairs (0, 4), (1, 5), .. of 4 bits
-            x[s][e] = v[BITS == 4 ? (e >> 1) + 4 * (e & 1) : e] * (scale * kLog2e);
+            x[s][e] = row.x[s][BITS == 4 ? (e >> 1) + 4 * (e & 1) : e] * (scale * kLog2e);
             most = fmaxf(most, fabsf(x[s][e]));
         }
     }

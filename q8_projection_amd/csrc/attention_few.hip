@@ -376,7 +376,9 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
                 }
                 half8 *words = query + n * (D / 32) * 128 + lane;
                 const auto dims = [&](int s) { return key_dims<BITS, D>(s, g); };
-                const float t = load_query<BITS, D / 32>(row, a.scale, dims, column_max, [&](int s, half8 hi, half8 lo) {
+                QueryRow<D / 32> q_row;
+                q_row.load(row, dims);
+                const float t = query_words<BITS>(q_row, a.scale, column_max, [&](int s, half8 hi, half8 lo) {
                     words[2 * s * 64] = hi, words[(2 * s + 1) * 64] = lo;
                 });
                 if (g == 0) to_scores[x] = t;

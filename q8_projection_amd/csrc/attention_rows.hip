@@ -48,49 +48,67 @@ struct RowsArgs {
 // Floats of a part: a row tile's sums, and (maximum, sum, -, -) for each lane of four waves.
 constexpr int slot_of(int d) { return kTile * (d + 8); }
 
-// The rows of tile `x` of a sequence's rows.
+// The rows of tile `x` of a sequence's rows (rows times heads is below 2^31: the outputs fit in memory).
 __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows &r, int x) {
-    const int64_t from = int64_t(x) * kTile / a.group;
-    const int64_t to = min((int64_t(x) + 1) * kTile + a.group - 1, int64_t(r.n) * a.group) / a.group;
+    const uint32_t group = a.group, from = uint32_t(x) * kTile / group;
+    const uint32_t to = min((uint32_t(x) + 1) * kTile + group - 1, uint32_t(r.n) * group) / group;
     return {static_cast<int>(r.first + from), static_cast<int>(to - from), static_cast<int>(r.at + from), r.end};
 }
 
 // The line of row tiles, sequence after sequence: with `whole` each is 1 long, the last one first and kv heads side
 // by side; else a kv head's row tiles follow one another, each about as long as the tiles of tokens that
-// it sees, which grow evenly from the sequence's first row tile to its last (fewer than kMaxLine row tiles).
-constexpr int kMaxLine = 1 << 16;
+// it sees, in sixteenths: these grow evenly from the sequence's first row tile to its last.
+constexpr int kLinePart = 16;
 struct Line {
-    bool whole;
-    int s0 = 0;          // sequences s0 .. s0 + 63 are the lanes'
+    // 64 sequences, a wave's: in LDS, for the registers are the products'
+    struct State {
+        int rows[4][64], tiles[64], first[64], step[64];
+        int64_t scan[64];
+    };
+    State &state;
+    int lane;
+    bool whole = true;
+    int s0 = 0;          // of sequences s0 .. s0 + 63
     int64_t before = 0;  // the line's place of the first of them
-    Rows rows;
-    int tiles, first, last;  // row tiles, and how much the first and the last see
-    int64_t scan;
 
-    // Place of a kv head's row tile x.
-    static __device__ __forceinline__ int64_t place(int x, int tiles, int first, int last) {
-        const int64_t more = max(last - first, 0);
-        return int64_t(x) * first + (tiles > 1 ? more * x * (x - 1) / (2 * (tiles - 1)) : 0);
+    // Place of a kv head's row tile x, the first one `first` long and each one `step` longer.
+    static __device__ __forceinline__ int64_t place(int x, int first, int step) {
+        return int64_t(x) * first + (int64_t(x) * (x - 1) >> 1) * step;
     }
-    __device__ __forceinline__ void look(const AttentionArgs &a, int lane) {
+    __device__ __forceinline__ void look(const AttentionArgs &a) {
         const int s = s0 + lane;
-        rows = Rows{0, 0, 0, 0};
+        Rows rows = {0, 0, 0, 0};
         if (s < a.c.sequences) rows = sequence_rows(a.c, s);
-        tiles = static_cast<int>((int64_t(rows.n) * a.group + kTile - 1) / kTile);
-        first = last = 0;
-        if (tiles) first = span_of(a, rows_of_tile(a, rows, 0)).n, last = span_of(a, rows_of_tile(a, rows, tiles - 1)).n;
-        scan = wave_scan(a.c.kv_heads * (whole ? int64_t(tiles) : place(tiles, tiles, first, last)));
-    }
-    // All of it; then at the first sequences again.
-    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int lane) {
-        int64_t all = 0;
-        for (s0 = 0; s0 < a.c.sequences; s0 += 64) {
-            look(a, lane);
-            all += lane_of(scan, 63);
+        const int tiles = static_cast<int>((uint32_t(rows.n) * uint32_t(a.group) + kTile - 1) / kTile);
+        int first = 0, step = 0;
+        if (tiles) {
+            first = kLinePart * span_of(a, rows_of_tile(a, rows, 0)).n;
+            step = max((kLinePart * span_of(a, rows_of_tile(a, rows, tiles - 1)).n - first) / max(tiles - 1, 1), 0);
         }
+        state.rows[0][lane] = rows.first, state.rows[1][lane] = rows.n, state.rows[2][lane] = rows.at, state.rows[3][lane] = rows.end;
+        state.tiles[lane] = tiles, state.first[lane] = first, state.step[lane] = step;
+    }
+    __device__ __forceinline__ int64_t scan(const AttentionArgs &a) {
+        const int n = state.tiles[lane];
+        const int64_t v = wave_scan(a.c.kv_heads * (whole ? int64_t(n) : place(n, state.first[lane], state.step[lane])));
+        state.scan[lane] = v;
+        return lane_of(v, 63);
+    }
+    // How long the line is, and which it is: whole row tiles if there are `many` or so many that their places would overflow.
+    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int64_t many) {
+        int64_t items = 0, all = 0;
+        for (s0 = 0; s0 < a.c.sequences; s0 += 64) {
+            look(a);
+            whole = true;
+            items += scan(a);
+            whole = false;
+            all += scan(a);
+        }
+        whole = items >= min(many, int64_t(1) << 16);
         s0 = 0;
-        if (a.c.sequences > 64) look(a, lane);
-        return all;
+        if (a.c.sequences > 64) look(a);
+        scan(a);
+        return whole ? items : all;
     }
     // The row tile at `at`, which is on the line and not before the last one found.
     struct Item {
@@ -98,42 +116,45 @@ struct Line {
         int64_t origin, length;
         Rows rows;
     };
-    __device__ __forceinline__ Item find(const AttentionArgs &a, int64_t at, int lane) {
+    __device__ __forceinline__ Item find(const AttentionArgs &a, int64_t at) {
         uint64_t above;
-        while (!(above = __ballot(before + scan > at)) && s0 + 64 < a.c.sequences) {
-            before += lane_of(scan, 63);
+        while (!(above = __ballot(before + state.scan[lane] > at)) && s0 + 64 < a.c.sequences) {
+            before += state.scan[63];
             s0 += 64;
-            look(a, lane);
+            look(a);
+            scan(a);
         }
         const int l = above ? __builtin_ctzll(above) : 63;
-        const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-        const int64_t begin = before + (l ? lane_of(scan, l - 1) : 0);
-        const int n = of(tiles);
+        const auto of = [&](const int(&v)[64]) { return __builtin_amdgcn_readfirstlane(v[l]); };
+        const int64_t begin = before + (l ? lane_of(state.scan[l - 1], 0) : 0);
+        const int n = of(state.tiles);
         Item it;
         it.s = s0 + l;
-        it.rows = Rows{of(rows.first), of(rows.n), of(rows.at), of(rows.end)};
+        it.rows = Rows{of(state.rows[0]), of(state.rows[1]), of(state.rows[2]), of(state.rows[3])};
         if (whole) {
-            const int64_t item = at - begin, x = item / a.c.kv_heads;
+            const uint32_t item = static_cast<uint32_t>(at - begin), x = item / uint32_t(a.c.kv_heads);
             it.head = static_cast<int>(item - x * a.c.kv_heads);
             it.tile = n - 1 - static_cast<int>(x);
             it.origin = at;
             it.length = 1;
             return it;
         }
-        const int f = of(first), e = of(last);
-        const int64_t head_length = place(n, n, f, e);
-        it.head = static_cast<int>((at - begin) / head_length);
-        const int64_t head_begin = begin + it.head * head_length, rest = at - head_begin;
+        const int first = of(state.first), step = of(state.step);
+        const int64_t head_length = place(n, first, step);
+        it.head = static_cast<int>(static_cast<float>(at - begin) / static_cast<float>(head_length));  // or one beside it
+        int64_t rest = at - begin - it.head * head_length;
+        if (rest < 0) --it.head, rest += head_length;
+        if (rest >= head_length) ++it.head, rest -= head_length;
         for (int x0 = 0;; x0 += 64) {  // the last row tile whose place is not past `rest`
-            const uint64_t past = __ballot(x0 + lane + 1 >= n || place(x0 + lane + 1, n, f, e) > rest);
+            const uint64_t past = __ballot(x0 + lane + 1 >= n || place(x0 + lane + 1, first, step) > rest);
             if (past) {
                 it.tile = x0 + __builtin_ctzll(past);
                 break;
             }
         }
-        const int64_t p = place(it.tile, n, f, e);
-        it.origin = head_begin + p;
-        it.length = place(it.tile + 1, n, f, e) - p;
+        const int64_t p = place(it.tile, first, step);
+        it.origin = at - rest + p;
+        it.length = first + int64_t(it.tile) * step;
         return it;
     }
 };
@@ -271,6 +292,7 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
     static_assert(kOperands * kGroups * 16 >= (kGroups - 1) * kTile * D * 4);
     __shared__ half8 operands[kGroups][kOperands];
     __shared__ float tops[256], sums[256];
+    __shared__ Line::State states[4 * kGroups];
     __shared__ uint32_t last;
     const AttentionArgs &a = f.a;
     const CacheArgs &c = a.c;
@@ -278,35 +300,38 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave & 3, group = wave >> 2;
     half8 *const keys = operands[group], *const values = keys + 2 * kKeys;
 
-    Line line;
-    line.whole = true;
-    int64_t all = line.measure(a, lane);
-    line.whole = all >= 2 * int64_t(f.workgroups) || all >= kMaxLine;
-    int64_t chunk = 1;
-    if (!line.whole) {
-        all = line.measure(a, lane);
-        chunk = max((all + f.workgroups - 1) / f.workgroups, int64_t(kMinTiles));
-    }
+    Line line = {states[wave], lane};
+    const int64_t all = line.measure(a, 2 * int64_t(f.workgroups));
+    const int64_t chunk = line.whole ? 1 : max((all + f.workgroups - 1) / f.workgroups, int64_t(kLinePart * kMinTiles));
 
     for (int64_t p = blockIdx.x; p * chunk < all; p += gridDim.x) {
         int64_t at = p * chunk;
         const int64_t stop = min(at + chunk, all);
         while (at < stop) {
-            const Line::Item it = line.find(a, at, lane);
+            const Line::Item it = line.find(a, at);
             const Rows r = it.rows, tile_rows = rows_of_tile(a, r, it.tile);
             const Span span = span_of(a, tile_rows);
             // this workgroup's share of the row tile
             const int64_t share_end = min(stop - it.origin, it.length);
-            const int from = static_cast<int>(int64_t(span.n) * (at - it.origin) / it.length);
-            const int to = static_cast<int>(int64_t(span.n) * share_end / it.length);
+            // (rounded, but a workgroup's end as the next one's beginning)
+            const auto tile_of = [&](int64_t part) {
+                return part == it.length ? span.n : min(static_cast<int>(double(span.n) * double(part) / double(it.length)), span.n);
+            };
+            const int from = tile_of(at - it.origin), to = tile_of(share_end);
             const bool alone = at == it.origin && share_end == it.length, begins = at == it.origin;
-            const int first = alone ? 0 : static_cast<int>(it.origin / chunk);
+            const int first = alone ? 0 : static_cast<int>(uint64_t(it.origin) / uint64_t(chunk));
             const int sharers = alone ? 1 : static_cast<int>((it.origin + it.length - 1) / chunk) - first + 1;
             at = it.origin + share_end;
             const int rows = r.n * a.group, row0 = it.tile * kTile, head = it.head;
             // tokens that any row of the tile sees, and those that every one does
             const int lo = a.window ? max(tile_rows.at - a.window + 1, 0) : 0, hi = min(tile_rows.at + tile_rows.n, r.end);
             const int all_lo = a.window ? max(tile_rows.at + tile_rows.n - a.window, 0) : 0, all_hi = min(tile_rows.at + 1, r.end);
+
+            // the lane's row; past the last one that one's query, whose scores are not looked at
+            const int x = row0 + wid * 32 + col;
+            const Where of_q = where(a, r, head, min(x, rows - 1));
+            QueryRow<kSteps> q_row;
+            q_row.load(a.q + of_q.row * a.q_ld + int64_t(of_q.head) * D, [&](int s) { return D / 2 * h + 8 * s; });
 
             // Pages of the tiles paged .. paged + 63, one a lane (-1: none).
             const int shift = c.page_shift - 5;
@@ -347,16 +372,12 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
             int page1 = page_of(begin + kGroups), page2 = page_of(begin + 2 * kGroups);
             kc.load(tile_in(begin, page0), kp);
             vc.load(tile_in(begin, page0), vp);
+            KeyCodes<BITS, D> kc1;
+            kc1.load(tile_in(begin + kGroups, page1), kp);
 
             half8 q_hi[kSteps], q_lo[kSteps];
-            const int x = row0 + wid * 32 + col;  // the lane's row
-            const float *row = nullptr;
-            if (x < rows) {
-                const Where q = where(a, r, head, x);
-                row = a.q + q.row * a.q_ld + int64_t(q.head) * D;
-            }
-            const float to_score = load_query<BITS, kSteps>(row, a.scale, [&](int s) { return D / 2 * h + 8 * s; }, column_max,
-                                                            [&](int s, half8 hi8, half8 lo8) { q_hi[s] = hi8, q_lo[s] = lo8; });
+            const float to_score =
+                query_words<BITS>(q_row, a.scale, column_max, [&](int s, half8 hi8, half8 lo8) { q_hi[s] = hi8, q_lo[s] = lo8; });
             float top = kNoMax, sum = 0.0f;
             f32x16 acc[kDims];
 #pragma unroll
@@ -387,11 +408,10 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
             clear_words(begin, page0);
 #pragma unroll
             for (int e = 0; e < kMine; ++e) kc.store(keys, e, wid, lane, kp), vc.store(values, e, wid, lane);
-            kc.load(tile_in(begin + kGroups, page1), kp);
+            kc.load(tile_in(begin + 2 * kGroups, page2), kp);
             vc.load(tile_in(begin + kGroups, page1), vp);
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) kc.store(keys + kKeys, e, wid, lane, kp);
-            kc.load(tile_in(begin + 2 * kGroups, page2), kp);
+            for (int e = 0; e < kMine; ++e) kc1.store(keys + kKeys, e, wid, lane, kp);
             clear_words(begin + kGroups, page1);
             __syncthreads();
             f32x16 z;
