@@ -296,11 +296,10 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
     __shared__ uint32_t last;
     const AttentionArgs &a = f.a;
     const CacheArgs &c = a.c;
-    const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave & 3, group = wave >> 2;
     half8 *const keys = operands[group], *const values = keys + 2 * kKeys;
 
-    Line line = {states[wave], lane};
+    Line line = {states[wave], static_cast<int>(threadIdx.x & 63)};
     const int64_t all = line.measure(a, 2 * int64_t(f.workgroups));
     const int64_t chunk = line.whole ? 1 : max((all + f.workgroups - 1) / f.workgroups, int64_t(kLinePart * kMinTiles));
 
@@ -308,6 +307,11 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
         int64_t at = p * chunk;
         const int64_t stop = min(at + chunk, all);
         while (at < stop) {
+            // (new to the compiler, which else makes what follows from them beforehand and keeps it in registers)
+            int lane = threadIdx.x & 63;
+            int64_t part_length = chunk;
+            asm volatile("" : "+v"(lane), "+s"(part_length));
+            const int h = lane >> 5, col = lane & 31;
             const Line::Item it = line.find(a, at);
             const Rows r = it.rows, tile_rows = rows_of_tile(a, r, it.tile);
             const Span span = span_of(a, tile_rows);
@@ -319,8 +323,8 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
             };
             const int from = tile_of(at - it.origin), to = tile_of(share_end);
             const bool alone = at == it.origin && share_end == it.length, begins = at == it.origin;
-            const int first = alone ? 0 : static_cast<int>(uint64_t(it.origin) / uint64_t(chunk));
-            const int sharers = alone ? 1 : static_cast<int>((it.origin + it.length - 1) / chunk) - first + 1;
+            const int first = alone ? 0 : static_cast<int>(uint64_t(it.origin) / uint64_t(part_length));
+            const int sharers = alone ? 1 : static_cast<int>((it.origin + it.length - 1) / part_length) - first + 1;
             at = it.origin + share_end;
             const int rows = r.n * a.group, row0 = it.tile * kTile, head = it.head;
             // tokens that any row of the tile sees, and those that every one does
