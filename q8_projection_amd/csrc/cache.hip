@@ -12,6 +12,8 @@
 //           lane holds all eight tokens of its dwords, and a block's values lie in the
 //           16 lanes of a DPP row.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "cache.h"
 #include "device.h"
@@ -52,14 +54,14 @@ __device__ __forceinline__ float scale_of(float span) {
     return t < 0x1p-14f ? low : up;
 }
 
-// rint(x / d), with r = 1 / d correctly rounded.  The first correction of x * r, which is up to
+// x / d, with r = 1 / d correctly rounded.  The first correction of x * r, which is up to
 // one and a half steps off, leaves one of the two neighbours of x / d, the second the correctly
 // rounded quotient (Markstein's theorem), and that is a half-integer only if the exact one is (x
 // has 24 bits, d six).  One correction alone rounds some quotients next to a half-integer wrongly.
-__device__ __forceinline__ float steps_of(float x, float d, float r) {
+__device__ __forceinline__ float quotient(float x, float d, float r) {
     float q = x * r;
     q = __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
-    return rintf(__builtin_fmaf(__builtin_fmaf(-q, d, x), r, q));
+    return __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
 }
 
 __device__ __forceinline__ float row_min(float v) {
@@ -73,26 +75,55 @@ __device__ __forceinline__ uint32_t half_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
-// A block's scale, its reciprocal, its zero point (4 bits) and its word.
+// A value of `lane` from the lane's four or sixteen neighbours that CTRL names.
+template <int CTRL>
+__device__ __forceinline__ int dpp_i32(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+
+// Whole numbers near rint(x / d) come as the bits of kMagic + x / d, rounded to the nearest there (ties to the
+// even, as kMagic is): kMagicBits + n, in order for all x, so that they are clamped as integers.
+constexpr float kMagic = 0x1.8p23f;
+constexpr int kMagicBits = 0x4b400000;
+
+// A block's scale, its reciprocal, and where codes begin: code 0 (4 bits) or 1 (8 bits) as x / d's bits.
 template <int BITS>
 struct Block {
-    float d, r, z;
+    float d, r;
+    int least;
 
     // low, high: the block's smallest value or 0, its largest or 0
     __device__ __forceinline__ void set(float low, float high) {
         d = scale_of<BITS>(BITS == 4 ? span_of(low, high) : fmaxf(high, -low));
         r = d > 0 ? 1.0f / d : 0.0f;
-        z = BITS == 4 ? fminf(steps_of(-low, d, r), 15.0f) : 0.0f;
+        least = BITS == 4 ? max(__builtin_bit_cast(int, kMagic - quotient(-low, d, r)), kMagicBits - 15) : kMagicBits - 127;
     }
     __device__ __forceinline__ uint32_t word() const {
-        return half_bits(d) | (BITS == 4 ? static_cast<uint32_t>(z) : 0u);
+        return half_bits(d) | (BITS == 4 ? static_cast<uint32_t>(kMagicBits - least) : 0u);
     }
     __device__ __forceinline__ uint32_t code(float x) const {
-        const float n = steps_of(x, d, r);
-        if (BITS == 4) return static_cast<uint32_t>(fminf(fmaxf(n + z, 0.0f), 15.0f));
-        return static_cast<uint32_t>(fminf(fmaxf(n, -127.0f), 127.0f) + 128.0f);
+        const int n = __builtin_bit_cast(int, quotient(x, d, r) + kMagic);
+        return static_cast<uint32_t>(min(max(n, least), least + (BITS == 4 ? 15 : 254)) - least + (BITS == 4 ? 0 : 1));
+    }
+    // that of lanes which CTRL names
+    template <int CTRL>
+    __device__ __forceinline__ Block of() const {
+        Block b;
+        b.d = dpp_f32<CTRL>(d), b.r = dpp_f32<CTRL>(r);
+        b.least = BITS == 4 ? dpp_i32<CTRL>(least) : least;
+        return b;
     }
 };
+
+template <typename Fn, int... I>
+__device__ __forceinline__ void each_of(Fn fn, std::integer_sequence<int, I...>) {
+    (fn(std::integral_constant<int, I>{}), ...);
+}
+// fn(0), .. fn(N - 1) with constants.
+template <int N, typename Fn>
+__device__ __forceinline__ void each(Fn fn) {
+    each_of(fn, std::make_integer_sequence<int, N>{});
+}
 
 // What a wave serves: a tile of a sequence, 64 dimensions of a kv head.
 struct Work {
@@ -100,36 +131,24 @@ struct Work {
 };
 
 template <int D>
-__device__ __forceinline__ Work work_of(const CacheArgs &c, int tiles) {
+__device__ __forceinline__ Work work_of(const CacheArgs &c, uint32_t tiles, uint32_t wave) {
     constexpr int kParts = D / 64;
-    const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * kWaves;
-    const int per = c.kv_heads * kParts;
-    const int64_t rest = wave / per;
-    const int u = static_cast<int>(wave - rest * per);
-    Work w;
-    w.s = static_cast<int>(rest / tiles);
-    w.tile = static_cast<int>(rest % tiles);
-    w.head = u / kParts;
-    w.part = u % kParts;
-    return w;
+    const uint32_t per = c.kv_heads * kParts, rest = wave / per, u = wave - rest * per, s = rest / tiles;
+    return {static_cast<int>(s), static_cast<int>(rest - s * tiles), static_cast<int>(u / kParts), static_cast<int>(u % kParts)};
 }
 
 // Tiles that the rows of one sequence can lie in: `rows` tokens anywhere.
 inline int64_t tiles_of(int rows) { return (int64_t(rows) + kTileTokens - 2) / kTileTokens + 1; }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int tiles) {
+__device__ __forceinline__ void append(const AppendArgs &a, const Work &w) {
     using T = Tile<BITS, D>;
-    const Work w = work_of<D>(a.c, tiles);
-    if (w.s >= a.c.sequences) return;
     const Rows rows = sequence_rows(a.c, w.s);
     const int t = max(rows.at, 0) / kTileTokens + w.tile;  // tile of the sequence
     const int t0 = t * kTileTokens;
     // tokens [lo, hi) of the tile are written
     const int lo = max(rows.at - t0, 0), hi = min(min(rows.at + rows.n, rows.end) - t0, kTileTokens);
     if (lo >= hi) return;
-    uint8_t *tile = tile_at<BITS, D>(a.c, w.s, t, w.head);
-    if (!tile) return;
     const int lane = threadIdx.x & 63;
     const int row0 = rows.first + (t0 - rows.at);  // row of the tile's token 0
     const int dim0 = w.part * 64;
@@ -155,53 +174,76 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) vx[n][i] = src[16 * i];
     }
+    uint8_t *tile = tile_at<BITS, D>(a.c, w.s, t, w.head);
+    if (!tile) return;
 
-    // Keys: a pass is 8 tokens.
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    // Keys: a pass is 8 tokens.  A block's scale is made by one of its four lanes: lane p of them has pass p's.
+    const auto pass_is = [&](int p) { return p * 8 < hi && p * 8 + 8 > lo; };
+    {
         float low = 0.0f, high = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) low = fminf(low, kx[p][e]), high = fmaxf(high, kx[p][e]);
-        low = fminf(low, dpp_f32<0xb1>(low)), high = fmaxf(high, dpp_f32<0xb1>(high));
-        low = fminf(low, dpp_f32<0x4e>(low)), high = fmaxf(high, dpp_f32<0x4e>(high));
-        Block<BITS> b;
-        b.set(low, high);
-        uint32_t code[2] = {0, 0};
+        for (int p = 0; p < 4; ++p) {
+            float l = 0.0f, h = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) code[BITS == 4 ? 0 : e / 4] |= b.code(kx[p][e]) << (BITS == 4 ? 4 * e : 8 * (e % 4));
-        const int tok = p * 8 + sub;
-        if (tok < lo || tok >= hi) continue;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(tile + tok * T::kRow + (dim0 + j * 8) * BITS / 8);
-        dst[0] = code[0];
-        if (BITS == 8) dst[1] = code[1];
-        if (j % 4 == 0)
-            reinterpret_cast<uint16_t *>(tile + T::kKeyWords)[key_word(tok, dim0 / 32 + j / 4, T::kBlocks)] =
-                static_cast<uint16_t>(b.word());
+            for (int e = 0; e < 8; ++e) l = fminf(l, kx[p][e]), h = fmaxf(h, kx[p][e]);
+            l = fminf(l, dpp_f32<0xb1>(l)), h = fmaxf(h, dpp_f32<0xb1>(h));
+            l = fminf(l, dpp_f32<0x4e>(l)), h = fmaxf(h, dpp_f32<0x4e>(h));
+            low = j % 4 == p ? l : low, high = j % 4 == p ? h : high;
+        }
+        Block<BITS> mine;
+        mine.set(low, high);
+        const int my_tok = j % 4 * 8 + sub;
+        if (my_tok >= lo && my_tok < hi)
+            reinterpret_cast<uint16_t *>(tile + T::kKeyWords)[key_word(my_tok, dim0 / 32 + j / 4, T::kBlocks)] =
+                static_cast<uint16_t>(mine.word());
+        each<4>([&](auto P) {
+            constexpr int p = P;
+            if (!pass_is(p)) return;
+            const Block<BITS> b = mine.template of<0x55 * p>();  // quad_perm [p,p,p,p]
+            uint32_t code[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) code[BITS == 4 ? 0 : e / 4] |= b.code(kx[p][e]) << (BITS == 4 ? 4 * e : 8 * (e % 4));
+            const int tok = p * 8 + sub;
+            if (tok < lo || tok >= hi) return;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(tile + tok * T::kRow + (dim0 + j * 8) * BITS / 8);
+            dst[0] = code[0];
+            if (BITS == 8) dst[1] = code[1];
+        });
     }
 
-    // Values: the eight tokens of dimensions 16 i + c.
+    // Values: the eight tokens of dimensions 16 i + c.  A block's scale is made by one of its 16 lanes: lane
+    // 2 n + u has that of the group's token n and the part's block u.
+    const auto token_is = [&](int n) { return hi - lo >= 8 || ((n - lo) & 7) < hi - lo; };  // a group's n, of any group
     uint32_t code[4][2] = {};
+    float low = 0.0f, high = 0.0f;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-        const int tok = g * 8 + n;
+        if (!token_is(n)) continue;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {  // block
-            const float low = row_min(fminf(fminf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
-            const float high = row_max(fmaxf(fmaxf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
-            Block<BITS> b;
-            b.set(low, high);
-#pragma unroll
-            for (int i = 2 * u; i < 2 * u + 2; ++i) {
-                const uint32_t q = b.code(vx[n][i]);
-                // 8 bits: byte 2 (n % 4) + n / 4
-                if (BITS == 4) code[i][0] |= q << (4 * n);
-                else code[i][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
-            }
-            if (c == n && tok >= lo && tok < hi)
-                reinterpret_cast<uint16_t *>(tile + T::kValueWords)[value_word(tok, dim0 / 32 + u)] =
-                    static_cast<uint16_t>(b.word());
+        for (int u = 0; u < 2; ++u) {
+            const float l = row_min(fminf(fminf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
+            const float h = row_max(fmaxf(fmaxf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
+            low = c == 2 * n + u ? l : low, high = c == 2 * n + u ? h : high;
         }
     }
+    Block<BITS> mine;
+    mine.set(low, high);
+    const int my_tok = g * 8 + (c >> 1);
+    if (my_tok >= lo && my_tok < hi)
+        reinterpret_cast<uint16_t *>(tile + T::kValueWords)[value_word(my_tok, dim0 / 32 + (c & 1))] =
+            static_cast<uint16_t>(mine.word());
+    each<16>([&](auto N) {
+        constexpr int n = N / 2, u = N % 2;
+        if (!token_is(n)) return;
+        const Block<BITS> b = mine.template of<0x150 + N>();  // row_newbcast
+#pragma unroll
+        for (int i = 2 * u; i < 2 * u + 2; ++i) {
+            const uint32_t q = b.code(vx[n][i]);
+            // 8 bits: byte 2 (n % 4) + n / 4
+            if (BITS == 4) code[i][0] |= q << (4 * n);
+            else code[i][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
+        }
+    });
     // the lane's tokens that are written, and what it keeps of those that are not
     const int first = max(lo - g * 8, 0), last = min(hi - g * 8, 8);
     if (first >= last) return;
@@ -233,10 +275,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int tile
 }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int tiles) {
+__device__ __forceinline__ void read(const ReadArgs &a, const Work &w) {
     using T = Tile<BITS, D>;
-    const Work w = work_of<D>(a.c, tiles);
-    if (w.s >= a.c.sequences) return;
     const Rows rows = sequence_rows(a.c, w.s);
     // the first row's token may lie before the sequence: its tile is then a negative one
     const int t = (rows.at >> 5) + w.tile, t0 = t * kTileTokens;
@@ -298,11 +338,27 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int tiles) {
     }
 }
 
+// The waves' work in turn: more waves than that only where most find nothing to do.
+constexpr int64_t kMaxBlocks = 1 << 20;
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, uint32_t tiles, uint32_t waves) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint32_t i = blockIdx.x * kWaves + wave; i < waves; i += gridDim.x * kWaves) append<BITS, D>(a, work_of<D>(a.c, tiles, i));
+}
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, uint32_t tiles, uint32_t waves) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint32_t i = blockIdx.x * kWaves + wave; i < waves; i += gridDim.x * kWaves) read<BITS, D>(a, work_of<D>(a.c, tiles, i));
+}
+
 template <typename Args, typename Kernel>
 hipError_t launch(Kernel kernel, const Args &a, int parts, hipStream_t stream) {
     const int64_t tiles = tiles_of(a.c.max_rows);
-    const int64_t waves = a.c.sequences * tiles * a.c.kv_heads * parts;
-    kernel<<<dim3(static_cast<uint32_t>((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a, static_cast<int>(tiles));
+    const int64_t waves = a.c.sequences * tiles * a.c.kv_heads * parts;  // below 2^31 by the limits of a call
+    const int64_t blocks = std::min((waves + kWaves - 1) / kWaves, kMaxBlocks);
+    kernel<<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(a, static_cast<uint32_t>(tiles), static_cast<uint32_t>(waves));
     return hipGetLastError();
 }
 
