@@ -8,9 +8,8 @@
 // writes the byte has both tokens, so that no atomics are needed.
 //   keys  : lane = 8 tokens x 8 dimensions: a block's 32 values lie in 4 lanes, whose
 //           smallest and largest meet in two DPP steps.
-//   values: lane (g, c) = tokens 8 g .. 8 g + 7 of dimensions 16 w + c, w = 0 .. 3: the
-//           lane holds all eight tokens of its dwords, and a block's values lie in the
-//           16 lanes of a DPP row.
+//   values: lane (g, b) = tokens 8 g .. 8 g + 7 of dimensions 4 b .. 4 b + 3: the lane holds
+//           all eight tokens of its dwords, and a block's values lie in 8 lanes.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -64,21 +63,43 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
     return __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
 }
 
-__device__ __forceinline__ float row_min(float v) {
-    v = fminf(v, dpp_f32<0xb1>(v));      // quad_perm [1,0,3,2]
-    v = fminf(v, dpp_f32<0x4e>(v));      // quad_perm [2,3,0,1]
-    v = fminf(v, dpp_f32<0x141>(v));     // row_half_mirror
-    return fminf(v, dpp_f32<0x140>(v));  // row_mirror
+// Smallest and largest over each 8 lanes.
+__device__ __forceinline__ float eight_min(float v) {
+    v = fminf(v, dpp_f32<0xb1>(v));          // quad_perm [1,0,3,2]
+    v = fminf(v, dpp_f32<0x4e>(v));          // quad_perm [2,3,0,1]
+    return fminf(v, dpp_f32<0x141>(v));      // row_half_mirror
+}
+__device__ __forceinline__ float eight_max(float v) {
+    v = fmaxf(v, dpp_f32<0xb1>(v));
+    v = fmaxf(v, dpp_f32<0x4e>(v));
+    return fmaxf(v, dpp_f32<0x141>(v));
+}
+
+// Where in a tile the codes are of the group g's tokens and dimensions 64 part + 4 b (.. + 3, each 16 bytes on).
+template <int BITS, int D>
+__device__ __forceinline__ uint32_t value_place(int part, int g, int b) {
+    const int w = b / 4, c = b % 4 * 4;  // dimension 16 w + c of the part
+    if (BITS == 4) return Tile<BITS, D>::kValues + ((part * 4 + g) * 16 + c) * 16 + w * 4;
+    return Tile<BITS, D>::kValues + (((part * 2 + w / 2) * 4 + g) * 16 + c) * 16 + w % 2 * 8;
 }
 
 __device__ __forceinline__ uint32_t half_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
-// A value of `lane` from the lane's four or sixteen neighbours that CTRL names.
 template <int CTRL>
 __device__ __forceinline__ int dpp_i32(int v) {
     return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+// The value of each eight lanes' lane N (row_newbcast of it to the row's first eight, of lane N + 8 to the others).
+template <int N>
+__device__ __forceinline__ int eight_lane(int v) {
+    const int low = __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0x3, false);
+    return __builtin_amdgcn_update_dpp(low, v, 0x158 + N, 0xf, 0xc, false);
+}
+template <int N>
+__device__ __forceinline__ float eight_lane(float v) {
+    return __builtin_bit_cast(float, eight_lane<N>(__builtin_bit_cast(int, v)));
 }
 
 // Whole numbers near rint(x / d) come as the bits of kMagic + x / d, rounded to the nearest there (ties to the
@@ -105,12 +126,19 @@ struct Block {
         const int n = __builtin_bit_cast(int, quotient(x, d, r) + kMagic);
         return static_cast<uint32_t>(min(max(n, least), least + (BITS == 4 ? 15 : 254)) - least + (BITS == 4 ? 0 : 1));
     }
-    // that of lanes which CTRL names
+    // another lane's
     template <int CTRL>
     __device__ __forceinline__ Block of() const {
         Block b;
         b.d = dpp_f32<CTRL>(d), b.r = dpp_f32<CTRL>(r);
         b.least = BITS == 4 ? dpp_i32<CTRL>(least) : least;
+        return b;
+    }
+    template <int N>
+    __device__ __forceinline__ Block of_eight() const {
+        Block b;
+        b.d = eight_lane<N>(d), b.r = eight_lane<N>(r);
+        b.least = BITS == 4 ? eight_lane<N>(least) : least;
         return b;
     }
 };
@@ -165,14 +193,13 @@ __device__ __forceinline__ void append(const AppendArgs &a, const Work &w) {
         kx[p][0] = x.x, kx[p][1] = x.y, kx[p][2] = x.z, kx[p][3] = x.w;
         kx[p][4] = y.x, kx[p][5] = y.y, kx[p][6] = y.z, kx[p][7] = y.w;
     }
-    const int g = lane >> 4, c = lane & 15;
+    const int g = lane >> 4, dims = lane & 15;
     float vx[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const int tok = min(max(g * 8 + n, lo), hi - 1);
-        const float *src = a.v + (row0 + tok) * a.v_ld + column + c;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vx[n][i] = src[16 * i];
+        const float4 x = *reinterpret_cast<const float4 *>(a.v + (row0 + tok) * a.v_ld + column + 4 * dims);
+        vx[n][0] = x.x, vx[n][1] = x.y, vx[n][2] = x.z, vx[n][3] = x.w;
     }
     uint8_t *tile = tile_at<BITS, D>(a.c, w.s, t, w.head);
     if (!tile) return;
@@ -211,66 +238,53 @@ __device__ __forceinline__ void append(const AppendArgs &a, const Work &w) {
         });
     }
 
-    // Values: the eight tokens of dimensions 16 i + c.  A block's scale is made by one of its 16 lanes: lane
-    // 2 n + u has that of the group's token n and the part's block u.
+    // Values.  A block's scale is made by one of its eight lanes: lane n of them has that of the group's token n.
     const auto token_is = [&](int n) { return hi - lo >= 8 || ((n - lo) & 7) < hi - lo; };  // a group's n, of any group
-    uint32_t code[4][2] = {};
+    constexpr int kWords = BITS / 4;  // dwords of a dimension's tokens
+    uint32_t code[4][kWords] = {};
     float low = 0.0f, high = 0.0f;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         if (!token_is(n)) continue;
+        float l = 0.0f, h = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float l = row_min(fminf(fminf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
-            const float h = row_max(fmaxf(fmaxf(vx[n][2 * u], vx[n][2 * u + 1]), 0.0f));
-            low = c == 2 * n + u ? l : low, high = c == 2 * n + u ? h : high;
-        }
+        for (int e = 0; e < 4; ++e) l = fminf(l, vx[n][e]), h = fmaxf(h, vx[n][e]);
+        l = eight_min(l), h = eight_max(h);
+        low = dims % 8 == n ? l : low, high = dims % 8 == n ? h : high;
     }
     Block<BITS> mine;
     mine.set(low, high);
-    const int my_tok = g * 8 + (c >> 1);
+    const int my_tok = g * 8 + dims % 8;
     if (my_tok >= lo && my_tok < hi)
-        reinterpret_cast<uint16_t *>(tile + T::kValueWords)[value_word(my_tok, dim0 / 32 + (c & 1))] =
-            static_cast<uint16_t>(mine.word());
-    each<16>([&](auto N) {
-        constexpr int n = N / 2, u = N % 2;
+        reinterpret_cast<uint16_t *>(tile + T::kValueWords)[value_word(my_tok, dim0 / 32 + dims / 8)] = static_cast<uint16_t>(mine.word());
+    each<8>([&](auto N) {
+        constexpr int n = N;
         if (!token_is(n)) return;
-        const Block<BITS> b = mine.template of<0x150 + N>();  // row_newbcast
+        const Block<BITS> b = mine.template of_eight<n>();
 #pragma unroll
-        for (int i = 2 * u; i < 2 * u + 2; ++i) {
-            const uint32_t q = b.code(vx[n][i]);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t q = b.code(vx[n][e]);
             // 8 bits: byte 2 (n % 4) + n / 4
-            if (BITS == 4) code[i][0] |= q << (4 * n);
-            else code[i][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
+            if (BITS == 4) code[e][0] |= q << (4 * n);
+            else code[e][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
         }
     });
     // the lane's tokens that are written, and what it keeps of those that are not
     const int first = max(lo - g * 8, 0), last = min(hi - g * 8, 8);
     if (first >= last) return;
-    uint32_t keep[2] = {0, 0};
+    uint32_t keep[kWords] = {};
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         if (n >= first && n < last) continue;
         if (BITS == 4) keep[0] |= 0xfu << (4 * n);
         else keep[(n & 3) >> 1] |= 0xffu << (16 * (n & 1) + 8 * (n >> 2));
     }
-    constexpr int kWords = BITS / 4;  // dwords of a dimension
-    uint32_t *dst = reinterpret_cast<uint32_t *>(tile + T::kValues) + ((w.part * kWords * 4 + g) * 16 + c) * 4;
+    uint8_t *dst = tile + value_place<BITS, D>(w.part, g, dims);
 #pragma unroll
-    for (int h = 0; h < kWords; ++h) {  // 16 bytes a lane: 4 dimensions of 4 bits, 2 of 8
-        uint4 *at = reinterpret_cast<uint4 *>(dst + h * 4 * 16 * 4);
-        uint4 out;
-        if (BITS == 4) out = make_uint4(code[0][0], code[1][0], code[2][0], code[3][0]);
-        else out = make_uint4(code[2 * h][0], code[2 * h][1], code[2 * h + 1][0], code[2 * h + 1][1]);
-        const uint32_t k0 = keep[0], k1 = BITS == 4 ? k0 : keep[1];
-        if (k0 | k1) {
-            const uint4 old = *at;
-            out.x = (out.x & ~k0) | (old.x & k0);
-            out.y = (out.y & ~k1) | (old.y & k1);
-            out.z = (out.z & ~k0) | (old.z & k0);
-            out.w = (out.w & ~k1) | (old.w & k1);
-        }
-        *at = out;
+    for (int e = 0; e < 4; ++e) {
+        uint32_t *at = reinterpret_cast<uint32_t *>(dst + 16 * e);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) at[i] = keep[i] ? (code[e][i] & ~keep[i]) | (at[i] & keep[i]) : code[e][i];
     }
 }
 
@@ -307,34 +321,33 @@ __device__ __forceinline__ void read(const ReadArgs &a, const Work &w) {
         *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
     }
 
-    const int g = lane >> 4, c = lane & 15;
+    const int g = lane >> 4, dims = lane & 15;
     constexpr int kWords = BITS / 4;
-    uint32_t code[kWords * 4] = {}, word[2][4] = {};
+    uint32_t code[4][kWords] = {};
+    uint4 words = make_uint4(0, 0, 0, 0);
     if (tile) {
+        const uint8_t *src = tile + value_place<BITS, D>(w.part, g, dims);
 #pragma unroll
-        for (int h = 0; h < kWords; ++h) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(tile + T::kValues +
-                                                            (((w.part * kWords + h) * 4 + g) * 16 + c) * 16);
-            code[4 * h] = x.x, code[4 * h + 1] = x.y, code[4 * h + 2] = x.z, code[4 * h + 3] = x.w;
-        }
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(tile + T::kValueWords + ((dim0 / 32 + u) * 4 + g) * 16);
-            word[u][0] = x.x, word[u][1] = x.y, word[u][2] = x.z, word[u][3] = x.w;
-        }
+            for (int i = 0; i < kWords; ++i) code[e][i] = reinterpret_cast<const uint32_t *>(src + 16 * e)[i];
+        words = *reinterpret_cast<const uint4 *>(tile + T::kValueWords + ((dim0 / 32 + dims / 8) * 4 + g) * 16);
     }
+    const uint32_t word[4] = {words.x, words.y, words.z, words.w};
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const int tok = g * 8 + n;
         if (tok < lo || tok >= hi) continue;
+        // words lie in pairs of tokens n, n + 4
+        const uint32_t m = word[n & 3] >> (16 * (n >> 2)) & 0xffffu;
+        const bool there = tile && tok < have;
+        float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // words lie in pairs of tokens n, n + 4
-            const uint32_t m = word[i >> 1][n & 3] >> (16 * (n >> 2)) & 0xffffu;
-            const uint32_t q = BITS == 4 ? code[i] >> (4 * n) & 15u
-                                         : code[2 * i + ((n & 3) >> 1)] >> (16 * (n & 1) + 8 * (n >> 2)) & 255u;
-            a.v[origin + tok * ld + 16 * i + c] = tok < have && tile ? value_of<BITS>(m, q) : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t q = BITS == 4 ? code[e][0] >> (4 * n) & 15u : code[e][(n & 3) >> 1] >> (16 * (n & 1) + 8 * (n >> 2)) & 255u;
+            x[e] = there ? value_of<BITS>(m, q) : 0.0f;
         }
+        *reinterpret_cast<float4 *>(a.v + origin + tok * ld + 4 * dims) = make_float4(x[0], x[1], x[2], x[3]);
     }
 }
 
