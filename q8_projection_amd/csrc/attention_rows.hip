@@ -32,11 +32,12 @@
 namespace q8 {
 namespace {
 
-constexpr int kTile = 128;     // query rows of a workgroup
 constexpr int kMinTiles = 16;  // tiles of a workgroup's part of the line, at least
 
-// Groups of four waves: 256 dimensions take twice the registers for queries and sums.
-constexpr int groups_of(int d) { return d == 256 ? 1 : 2; }
+constexpr int kGroups = 2;  // of waves
+// A group's waves, of 32 query rows each: 256 dimensions take twice the registers for queries and sums.
+constexpr int waves_of(int d) { return d == 256 ? 2 : 4; }
+constexpr int rows_of(int d) { return 32 * waves_of(d); }  // query rows of a workgroup, a row tile
 
 struct RowsArgs {
     AttentionArgs a;
@@ -45,13 +46,14 @@ struct RowsArgs {
     float *parts;       // [2 workgroups][slot]
 };
 
-// Floats of a part: a row tile's sums, and (maximum, sum, -, -) for each lane of four waves.
-constexpr int slot_of(int d) { return kTile * (d + 8); }
+// Floats of a part: a row tile's sums, and (maximum, sum, -, -) for each lane of a group.
+constexpr int slot_of(int d) { return rows_of(d) * (d + 8); }
 
 // The rows of tile `x` of a sequence's rows (rows times heads is below 2^31: the outputs fit in memory).
+template <int TILE>
 __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows &r, int x) {
-    const uint32_t group = a.group, from = uint32_t(x) * kTile / group;
-    const uint32_t to = min((uint32_t(x) + 1) * kTile + group - 1, uint32_t(r.n) * group) / group;
+    const uint32_t group = a.group, from = uint32_t(x) * TILE / group;
+    const uint32_t to = min((uint32_t(x) + 1) * TILE + group - 1, uint32_t(r.n) * group) / group;
     return {static_cast<int>(r.first + from), static_cast<int>(to - from), static_cast<int>(r.at + from), r.end};
 }
 
@@ -59,6 +61,7 @@ __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows 
 // by side; else a kv head's row tiles follow one another, each about as long as the tiles of tokens that
 // it sees, in sixteenths: these grow evenly from the sequence's first row tile to its last.
 constexpr int kLinePart = 16;
+template <int TILE>
 struct Line {
     // 64 sequences, a wave's: in LDS, for the registers are the products'
     struct State {
@@ -79,11 +82,11 @@ struct Line {
         const int s = s0 + lane;
         Rows rows = {0, 0, 0, 0};
         if (s < a.c.sequences) rows = sequence_rows(a.c, s);
-        const int tiles = static_cast<int>((uint32_t(rows.n) * uint32_t(a.group) + kTile - 1) / kTile);
+        const int tiles = static_cast<int>((uint32_t(rows.n) * uint32_t(a.group) + TILE - 1) / TILE);
         int first = 0, step = 0;
         if (tiles) {
-            first = kLinePart * span_of(a, rows_of_tile(a, rows, 0)).n;
-            step = max((kLinePart * span_of(a, rows_of_tile(a, rows, tiles - 1)).n - first) / max(tiles - 1, 1), 0);
+            first = kLinePart * span_of(a, rows_of_tile<TILE>(a, rows, 0)).n;
+            step = max((kLinePart * span_of(a, rows_of_tile<TILE>(a, rows, tiles - 1)).n - first) / max(tiles - 1, 1), 0);
         }
         state.rows[0][lane] = rows.first, state.rows[1][lane] = rows.n, state.rows[2][lane] = rows.at, state.rows[3][lane] = rows.end;
         state.tiles[lane] = tiles, state.first[lane] = first, state.step[lane] = step;
@@ -159,15 +162,16 @@ struct Line {
     }
 };
 
-// What a wave turns into operands of a tile: a quarter of the keys' codes, and of the values'.  An operand of the
+// What a wave turns into operands of a tile: its group's share of the keys' codes, and of the values'.  An operand of the
 // scores is 16 dimensions of the tile's tokens: step s has dimensions D / 2 h + 8 s + e; wave w makes steps
 // kMine w + ..
 template <int BITS, int D>
 struct KeyCodes {
     using T = Tile<BITS, D>;
-    static constexpr int kMine = D / 64;
+    static constexpr int kMine = D / 16 / waves_of(D);
     static constexpr int kDwords = kMine * BITS / 4;  // a lane
-    uint32_t x[kDwords], w;
+    static constexpr int kBlocks = (kMine + 3) / 4;
+    uint32_t x[kDwords], w[kBlocks];
 
     // where a lane's codes and word are, and which half of the word's pair is its token's
     struct Place {
@@ -193,12 +197,13 @@ struct KeyCodes {
                 for (int e = 0; e < 4; ++e) x[4 * u + e] = v[e];
             }
         }
-        w = load1(tile, p.word, 0);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) w[b] = load1(tile, p.word, 4 * b);
     }
     // operand e to [step][lane]
     __device__ __forceinline__ void store(half8 *keys, int e, int wid, int lane, const Place &p) const {
         Scales<BITS> s;
-        s.set(__builtin_amdgcn_perm(w, w, p.half));
+        s.set(__builtin_amdgcn_perm(w[e / 4], w[e / 4], p.half));
         half8 v;
         if constexpr (BITS == 4) v = values_of(x[e], s, s, s, s);
         else v = values_of(x[2 * e], x[2 * e + 1], s, s, s, s);
@@ -207,13 +212,13 @@ struct KeyCodes {
 };
 
 // An operand (u, d) of the sums is 32 dimensions of tokens 16 u + 8 h + e; its row c is dimension
-// out_dim(c, d).  Wave w makes operands (w / 2, kMine (w % 2) + ..).
+// out_dim(c, d).  Half of a group's waves make operands of u = 0, half of u = 1, kMine each.
 template <int BITS, int D>
 struct ValueCodes {
     using T = Tile<BITS, D>;
-    static constexpr int kMine = D / 64;
+    static constexpr int kMine = D / 16 / waves_of(D), kHalf = waves_of(D) / 2;
     static constexpr int kDwords = kMine * BITS / 4;
-    static constexpr int kBlocks = BITS == 4 && D == 256 ? 2 : BITS == 8 && D == 256 ? 2 : 1;
+    static constexpr int kBlocks = D == 256 ? kMine / 2 : 1;
     // A unit of the layout is 64 (4 bits) or 32 dimensions: 16 chunks of kIn times 16.  The rows' halves are
     // units side by side, or (one unit) dimensions of one.
     static constexpr int kUnit = BITS == 4 ? 64 : 32, kIn = kUnit / 16;
@@ -229,7 +234,7 @@ struct ValueCodes {
         uint32_t code, word;
     };
     static __device__ __forceinline__ Place place(uint32_t wid, uint32_t h, uint32_t c) {
-        const uint32_t a = 2 * (wid >> 1) + h, d = kMine * (wid & 1);
+        const uint32_t a = 2 * (wid / kHalf) + h, d = kMine * (wid % kHalf);
         const uint32_t unit = kOneUnit ? 0 : 2 * (d / kIn) + (c >> 4), in = kOneUnit ? 2 * d + (c >> 4) : d % kIn;
         // blocks of 32 dimensions: two a unit of 4 bits, one of 8
         const uint32_t block = BITS == 4 ? 2 * unit + in / 2 : unit;
@@ -241,7 +246,7 @@ struct ValueCodes {
         } else if constexpr (kDwords == 2) {
             const u32x2 v = load2(tile, p.code, 0);
             x[0] = v.x, x[1] = v.y;
-        } else {  // 16 bytes of a unit; a wave's second ones lie two units on
+        } else {  // 16 bytes of a unit; a wave's next ones lie two units on
 #pragma unroll
             for (int q = 0; q < kDwords / 4; ++q) {
                 const u32x4 v = load4(tile, p.code, q * (2 * 4 * 16 * 16));
@@ -249,19 +254,18 @@ struct ValueCodes {
                 for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
             }
         }
-        constexpr uint32_t kNext = BITS == 4 ? 1 : 2;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) w[b] = load4(tile, p.word, b * kNext * 64);
+        for (int b = 0; b < kBlocks; ++b) w[b] = load4(tile, p.word, (BITS == 4 ? b / 2 * 4 + b % 2 : 2 * b) * 64);
     }
     // operand e to [u][d][lane]
     __device__ __forceinline__ void store(half8 *values, int e, int wid, int lane) const {
         Scales<BITS> s[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) s[p].set(w[kBlocks == 2 ? e / 2 : 0][p]);
+        for (int p = 0; p < 4; ++p) s[p].set(w[kBlocks > 1 ? e / 2 : 0][p]);
         half8 v;
         if constexpr (BITS == 4) v = values_of(x[e], s[0], s[1], s[2], s[3]);
         else v = values_of(x[2 * e], x[2 * e + 1], s[0], s[1], s[2], s[3]);
-        values[((wid >> 1) * (D / 32) + (wid & 1) * kMine + e) * 64 + lane] = v;
+        values[(wid / kHalf * (D / 32) + wid % kHalf * kMine + e) * 64 + lane] = v;
     }
 };
 
@@ -282,24 +286,24 @@ __device__ __forceinline__ float largest(const f32x16 &z) {
 }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(RowsArgs f) {
+__global__ __launch_bounds__(64 * waves_of(D) * kGroups, waves_of(D) / 2) void rows_kernel(RowsArgs f) {
     using V = ValueCodes<BITS, D>;
-    constexpr int kSteps = D / 16, kDims = D / 32, kMine = D / 64, kSlot = slot_of(D);
-    constexpr int kGroups = groups_of(D);
+    constexpr int kSteps = D / 16, kDims = D / 32, kSlot = slot_of(D);
+    constexpr int kWaves = waves_of(D), kTile = rows_of(D), kMine = V::kMine;
     // A group's operands: keys, keys of the next tile, values, values of the next tile.  As large as the sums of
     // a group's waves, which meet there.
     constexpr int kKeys = kSteps * 64, kValues = 2 * kDims * 64, kOperands = 2 * (kKeys + kValues);
-    static_assert(kOperands * kGroups * 16 >= (kGroups - 1) * kTile * D * 4);
+    static_assert(kOperands * kGroups * 16 >= kTile * D * 4);
     __shared__ half8 operands[kGroups][kOperands];
-    __shared__ float tops[256], sums[256];
-    __shared__ Line::State states[4 * kGroups];
+    __shared__ float tops[64 * kWaves], sums[64 * kWaves];
+    __shared__ typename Line<kTile>::State states[kWaves * kGroups];
     __shared__ uint32_t last;
     const AttentionArgs &a = f.a;
     const CacheArgs &c = a.c;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave & 3, group = wave >> 2;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave % kWaves, group = wave / kWaves;
     half8 *const keys = operands[group], *const values = keys + 2 * kKeys;
 
-    Line line = {states[wave], static_cast<int>(threadIdx.x & 63)};
+    Line<kTile> line = {states[wave], static_cast<int>(threadIdx.x & 63)};
     const int64_t all = line.measure(a, 2 * int64_t(f.workgroups));
     const int64_t chunk = line.whole ? 1 : max((all + f.workgroups - 1) / f.workgroups, int64_t(kLinePart * kMinTiles));
 
@@ -312,8 +316,8 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
             int64_t part_length = chunk;
             asm volatile("" : "+v"(lane), "+s"(part_length));
             const int h = lane >> 5, col = lane & 31;
-            const Line::Item it = line.find(a, at);
-            const Rows r = it.rows, tile_rows = rows_of_tile(a, r, it.tile);
+            const typename Line<kTile>::Item it = line.find(a, at);
+            const Rows r = it.rows, tile_rows = rows_of_tile<kTile>(a, r, it.tile);
             const Span span = span_of(a, tile_rows);
             // this workgroup's share of the row tile
             const int64_t share_end = min(stop - it.origin, it.length);
@@ -363,7 +367,7 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
                 if (pg >= 0 && t0 >= lo && t0 + kTileTokens <= hi) return;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int t = t0 + 16 * (wid >> 1) + 8 * h + q;
+                    const int t = t0 + 16 * (wid / V::kHalf) + 8 * h + q;
                     const uint32_t there = (t >= lo && t < hi ? 0xffffu : 0u) | (t + 4 >= lo && t + 4 < hi ? 0xffff0000u : 0u);
 #pragma unroll
                     for (auto &w : vc.w) w[q] = pg < 0 ? 0u : w[q] & there;
@@ -480,7 +484,7 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
                 __syncthreads();
             }
 
-            if constexpr (kGroups == 2) {  // the other group's sums, lane by lane
+            {  // the other group's sums, lane by lane
                 f32x4 *meet = reinterpret_cast<f32x4 *>(&operands[0][0]) + wid * (kDims * 4 * 64) + lane;
                 if (group == 1) {
 #pragma unroll
@@ -515,7 +519,7 @@ __global__ __launch_bounds__(256 * groups_of(D), groups_of(D)) void rows_kernel(
                 // place is.
                 const __amdgpu_buffer_rsrc_t parts = parts_of(f.parts, 2 * f.workgroups * kSlot);
                 const auto part = [&](int i, bool begins) {
-                    return static_cast<uint32_t>(2 * i + begins) * kSlot + wid * (kSlot / 4) + 4 * lane;
+                    return static_cast<uint32_t>(2 * i + begins) * kSlot + wid * (kSlot / kWaves) + 4 * lane;
                 };
                 if (group == 0) {
                     const uint32_t mine = part(static_cast<int>(p), begins);
@@ -578,10 +582,10 @@ int rows_workgroups() { return device_info().cus; }
 template <int BITS, int D>
 hipError_t run(const RowsArgs &f, hipStream_t stream) {
     // a workgroup for each row tile there may be, unless there are very many
-    const int64_t row_tiles = (int64_t(f.a.c.max_rows) * f.a.group + kTile - 1) / kTile;
+    const int64_t row_tiles = (int64_t(f.a.c.max_rows) * f.a.group + rows_of(D) - 1) / rows_of(D);
     const int64_t most = std::max<int64_t>(f.workgroups, f.a.c.sequences * f.a.c.kv_heads * row_tiles);
     const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(most, 32 * int64_t(f.workgroups))));
-    rows_kernel<BITS, D><<<grid, 256 * groups_of(D), 0, stream>>>(f);
+    rows_kernel<BITS, D><<<grid, 64 * waves_of(D) * kGroups, 0, stream>>>(f);
     return hipGetLastError();
 }
 
