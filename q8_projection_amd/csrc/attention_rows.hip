@@ -32,7 +32,7 @@
 namespace q8 {
 namespace {
 
-constexpr int kMinTiles = 16;  // tiles of a workgroup's part of the line, at least
+constexpr int kMinTiles = 12;  // tiles of a workgroup's part of the line, at least
 
 constexpr int kGroups = 2;  // of waves
 // A group's waves, of 32 query rows each: 256 dimensions take twice the registers for queries and sums.
@@ -61,8 +61,12 @@ __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows 
 // by side; else a kv head's row tiles follow one another, each about as long as the tiles of tokens that
 // it sees, in sixteenths: these grow evenly from the sequence's first row tile to its last.
 constexpr int kLinePart = 16;
-template <int TILE>
+// What a row tile costs besides its tiles (queries, first tiles and ends of the pipeline, the output), in tiles of
+// tokens; a part that does not end there costs as much and a join.
+constexpr int cost_of(int d) { return d == 64 ? 24 : d == 128 ? 12 : 18; }
+template <int D>
 struct Line {
+    static constexpr int TILE = rows_of(D), kCost = cost_of(D), kJoin = 2 * kCost;
     // 64 sequences, a wave's: in LDS, for the registers are the products'
     struct State {
         int rows[4][64], tiles[64], first[64], step[64];
@@ -85,8 +89,8 @@ struct Line {
         const int tiles = static_cast<int>((uint32_t(rows.n) * uint32_t(a.group) + TILE - 1) / TILE);
         int first = 0, step = 0;
         if (tiles) {
-            first = kLinePart * span_of(a, rows_of_tile<TILE>(a, rows, 0)).n;
-            step = max((kLinePart * span_of(a, rows_of_tile<TILE>(a, rows, tiles - 1)).n - first) / max(tiles - 1, 1), 0);
+            first = kLinePart * (span_of(a, rows_of_tile<TILE>(a, rows, 0)).n + kCost);
+            step = max((kLinePart * (span_of(a, rows_of_tile<TILE>(a, rows, tiles - 1)).n + kCost) - first) / max(tiles - 1, 1), 0);
         }
         state.rows[0][lane] = rows.first, state.rows[1][lane] = rows.n, state.rows[2][lane] = rows.at, state.rows[3][lane] = rows.end;
         state.tiles[lane] = tiles, state.first[lane] = first, state.step[lane] = step;
@@ -97,17 +101,25 @@ struct Line {
         state.scan[lane] = v;
         return lane_of(v, 63);
     }
-    // How long the line is, and which it is: whole row tiles if there are `many` or so many that their places would overflow.
-    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int64_t many) {
+    // How long the line is, and which it is: row tiles are whole if that takes no longer than equal parts, which
+    // are joined (or if they are so many that their places would overflow).
+    __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int workgroups) {
         int64_t items = 0, all = 0;
+        float longest = 0.0f, shortest = 3.0e38f;
         for (s0 = 0; s0 < a.c.sequences; s0 += 64) {
             look(a);
+            const int n = state.tiles[lane];
+            const float first = static_cast<float>(state.first[lane]), last = first + static_cast<float>(state.step[lane]) * static_cast<float>(n - 1);
+            longest = fmaxf(longest, wave_max(n ? last : 0.0f));
+            shortest = fminf(shortest, -wave_max(n ? -first : -3.0e38f));
             whole = true;
             items += scan(a);
             whole = false;
             all += scan(a);
         }
-        whole = items >= min(many, int64_t(1) << 16);
+        // Whole, the longest first: the workgroups that have no row tile in the last round wait for the shortest.
+        const float per = static_cast<float>(items) / static_cast<float>(workgroups), part = static_cast<float>(all) / static_cast<float>(workgroups);
+        whole = items >= 1 << 16 || fmaxf(longest, part + (ceilf(per) - per) * shortest) <= part + kLinePart * kJoin;
         s0 = 0;
         if (a.c.sequences > 64) look(a);
         scan(a);
@@ -296,15 +308,15 @@ __global__ __launch_bounds__(64 * waves_of(D) * kGroups, waves_of(D) / 2) void r
     static_assert(kOperands * kGroups * 16 >= kTile * D * 4);
     __shared__ half8 operands[kGroups][kOperands];
     __shared__ float tops[64 * kWaves], sums[64 * kWaves];
-    __shared__ typename Line<kTile>::State states[kWaves * kGroups];
+    __shared__ typename Line<D>::State states[kWaves * kGroups];
     __shared__ uint32_t last;
     const AttentionArgs &a = f.a;
     const CacheArgs &c = a.c;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wid = wave % kWaves, group = wave / kWaves;
     half8 *const keys = operands[group], *const values = keys + 2 * kKeys;
 
-    Line<kTile> line = {states[wave], static_cast<int>(threadIdx.x & 63)};
-    const int64_t all = line.measure(a, 2 * int64_t(f.workgroups));
+    Line<D> line = {states[wave], static_cast<int>(threadIdx.x & 63)};
+    const int64_t all = line.measure(a, f.workgroups);
     const int64_t chunk = line.whole ? 1 : max((all + f.workgroups - 1) / f.workgroups, int64_t(kLinePart * kMinTiles));
 
     for (int64_t p = blockIdx.x; p * chunk < all; p += gridDim.x) {
@@ -316,7 +328,7 @@ __global__ __launch_bounds__(64 * waves_of(D) * kGroups, waves_of(D) / 2) void r
             int64_t part_length = chunk;
             asm volatile("" : "+v"(lane), "+s"(part_length));
             const int h = lane >> 5, col = lane & 31;
-            const typename Line<kTile>::Item it = line.find(a, at);
+            const typename Line<D>::Item it = line.find(a, at);
             const Rows r = it.rows, tile_rows = rows_of_tile<kTile>(a, r, it.tile);
             const Span span = span_of(a, tile_rows);
             // this workgroup's share of the row tile
@@ -539,38 +551,50 @@ __global__ __launch_bounds__(64 * waves_of(D) * kGroups, waves_of(D) / 2) void r
                     if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 }
                 __syncthreads();
-                if (group == 0 && last) {  // all of them, in the workgroups' order
+                if (last) {  // all of them, in the workgroups' order: half of the dimensions a group, the next part under way
+                    constexpr int kHalf = kDims / 2, kLoads = kHalf * 4;
+                    f32x4 o[kLoads], next[kLoads], st, next_st;
+                    const auto load = [&](int i, f32x4(&to)[kLoads], f32x4 &to_st) {
+                        const uint32_t from_part = part(first + i, i == 0);
+                        to_st = load_part(parts, from_part + kDims * 1024);
+#pragma unroll
+                        for (int e = 0; e < kLoads; ++e) to[e] = load_part(parts, from_part + (group * kLoads + e) * 256);
+                    };
+                    load(0, o, st);
                     top = kNoMax;
                     sum = 0.0f;
 #pragma unroll
-                    for (int d = 0; d < kDims; ++d)
+                    for (int d = 0; d < kHalf; ++d)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
                     for (int i = 0; i < sharers; ++i) {
-                        const uint32_t from_part = part(first + i, i == 0);
-                        const f32x4 st = load_part(parts, from_part + kDims * 1024);
-                        f32x4 o[kDims * 4];
-#pragma unroll
-                        for (int e = 0; e < kDims * 4; ++e) o[e] = load_part(parts, from_part + e * 256);
+                        load(min(i + 1, sharers - 1), next, next_st);
                         const float now = fmaxf(top, st.x), keep = exp2_of(top - now), more = exp2_of(st.x - now);
                         top = now;
                         sum = sum * keep + st.y * more;
 #pragma unroll
-                        for (int d = 0; d < kDims; ++d)
+                        for (int d = 0; d < kHalf; ++d)
 #pragma unroll
                             for (int e = 0; e < 16; ++e) acc[d][e] = acc[d][e] * keep + o[4 * d + e / 4][e % 4] * more;
+#pragma unroll
+                        for (int e = 0; e < kLoads; ++e) o[e] = next[e];
+                        st = next_st;
                     }
                 }
             }
-            if (x < rows && group == 0 && (alone || last)) {
+            // (what the wave has: all dimensions or its group's half)
+            const int from_d = alone ? 0 : group * (kDims / 2), end_d = alone ? kDims : kDims / 2;
+            if (x < rows && (alone ? group == 0 : last != 0)) {
                 constexpr float kScale = Scales<BITS>::kUp;
                 const Where to_row = where(a, r, head, x);
 #pragma unroll
-                for (int d = 0; d < kDims; ++d)
+                for (int d = 0; d < kDims; ++d) {
+                    if (d >= end_d) break;
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
-                        write_row<D>(a, to_row, V::out_dim(2 * e + 4 * h, d),
+                        write_row<D>(a, to_row, V::out_dim(2 * e + 4 * h, from_d + d),
                                      f32x4{acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]} * kScale, sum, top);
+                }
             }
             __syncthreads();  // LDS is free again
         }
