@@ -141,7 +141,12 @@ int64_t q8_attention_workspace_bytes(const q8_cache *cache, const q8_cache_batch
     a.c = args_of(cache, batch);
     a.heads = static_cast<int>(heads);
     a.group = a.heads / a.c.kv_heads;
-    return few(a, cache->head_dim) ? q8::few_workspace(cache->head_dim, a) : q8::rows_workspace(cache->head_dim);
+    const int dim = cache->head_dim;
+    if (few(a, dim)) return q8::few_workspace(dim, a);
+    // as large as for any call of few rows, so that the largest call's serves them too
+    a.c.max_rows = q8::few_rows(dim);
+    a.group = 1;
+    return std::max(q8::few_workspace(dim, a), q8::rows_workspace(dim));
 }
 
 q8_status q8_attention(const q8_cache *cache, const q8_cache_batch *batch, const float *q, int64_t q_ld,
