@@ -8,6 +8,11 @@
 // Codes go from memory to registers, in the order of the matrix cores' operands, and become binary16
 // values there.
 //
+// Measured, 4 bits, 32 heads of 8 kv heads and 128 dimensions: one sequence of 131071 tokens 39 us, 151 MB at 3.8 TB/s; a
+// batch of 64 of up to 8192 tokens 76 us, 294 MB at 3.9 TB/s.  A tile takes a wave some 370 vector instructions (codes
+// to values most of all, then weights) and 32 products: it is their issue that bounds long calls, and short ones the chain
+// of some 8 us from the lengths to the table, the codes, the waves' meeting and the join.
+//
 // v_mfma_f32_16x16x32_f16, as its lanes hold it (lane = 16 g + c):
 //   A: row c, depth 8 g + e (e = 0 .. 7);  B: column c, depth 8 g + e;  C: column c, rows 4 g + r
 // Scores: row c of half i is token 8 (c / 4) + 4 i + c % 4 of a tile, so that lane (g, c) gets row c's

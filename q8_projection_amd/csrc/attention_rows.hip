@@ -2,11 +2,11 @@
 // of large groups): bound by the matrix cores.
 //
 // A workgroup takes a tile of 128 query rows of one sequence and kv head (a token's query heads side by
-// side).  Four waves, with 32 rows each, walk over the tiles of 32 tokens that the rows see; four more over
-// every second of them, with the same rows, and their sums meet in LDS (256 dimensions: four waves alone, for the
-// registers).  So a SIMD has two waves, one's softmax beside the other's products, and a row tile is done in half the
-// time, which is what evens out causal prompts.  Keys and values become binary16 once for four waves: each
-// turns a quarter of a tile's codes into operands of the matrix cores and leaves them in LDS in the order in
+// side; 64 rows of 256 dimensions, for the registers).  A group of waves, with 32 rows each, walks over the tiles of 32
+// tokens that the rows see; a second group over every second of them, with the same rows, and their sums meet in LDS.
+// So a SIMD has two waves (256 dimensions: one), one's softmax beside the other's products, and a row tile is
+// done in half the time, which is what evens out causal prompts.  Keys and values become binary16 once for a group:
+// each wave turns its share of a tile's codes into operands of the matrix cores and leaves them in LDS in the order in
 // which a wave takes them (no bank conflicts).  A stage makes
 //   the weights of tile t from its scores,  the scores of the tile after it,  the sums of tile t,
 //   the operands of the keys two tiles on and the values one tile on,
@@ -15,9 +15,15 @@
 // more room for other instructions beside them than the 16 x 16 x 32 ones, which take twice as many
 // operands from the registers for the same work.
 //
-// Many row tiles are taken whole, a prompt's last ones, which see most, first.  Fewer than two for each
-// workgroup that the chip holds stand in one line, sequence after sequence, of which every workgroup
-// takes an equal part; a row tile that several share is joined by the last of them, in the order of the workgroups.
+// Row tiles are taken whole, a prompt's last ones, which see most, first; or they stand in one line, sequence after
+// sequence, of which every workgroup takes an equal part, and a row tile that several share is joined by the last
+// of them, in the order of the workgroups.  What is estimated to take longer is not taken (Line::measure).
+//
+// Measured: a prompt of 2048 tokens, 32 heads of 8 kv heads and 128 dimensions, 4 bits: 89 us for 34 GFLOP, 0.78 PFLOP/s of
+// binary16 products with both words (a large library product reaches 1.1); two chunks of 512 tokens after 16384: 384 us for 196
+// GFLOP, 1.02 PFLOP/s.  A stage takes some 3500 cycles of 1.9 GHz, 2048 of which the matrix cores work; the rest is the issue
+// port, which a product takes for half of its time and each weight (an exponential, two words) and code for its own.
+// Beside the stages a row tile takes some 12 us: its queries, the first tiles' way through memory, the output.
 //
 // v_mfma_f32_32x32x16_f16, as its lanes hold it (lane = 32 h + c):
 //   A: row c, depth 8 h + e (e = 0 .. 7);  B: column c, depth 8 h + e;
@@ -32,10 +38,13 @@
 namespace q8 {
 namespace {
 
-constexpr int kMinTiles = 12;  // tiles of a workgroup's part of the line, at least
+// Tiles of a workgroup's part of the line, at least.  64 rows after 3000 tokens: 44.6 us, at 8 48.0, at 16 47.1; 100 after 9000
+// of 256 dimensions: 71.6, at 8 76.9, at 16 77.6.
+constexpr int kMinTiles = 12;
 
 constexpr int kGroups = 2;  // of waves
-// A group's waves, of 32 query rows each: 256 dimensions take twice the registers for queries and sums.
+// A group's waves, of 32 query rows each: 256 dimensions take twice the registers for queries and sums.  (One group of four
+// waves there: chunks of 700 tokens in a window of 1024 82 us, with two of two 77.)
 constexpr int waves_of(int d) { return d == 256 ? 2 : 4; }
 constexpr int rows_of(int d) { return 32 * waves_of(d); }  // query rows of a workgroup, a row tile
 
@@ -102,7 +111,9 @@ struct Line {
         return lane_of(v, 63);
     }
     // How long the line is, and which it is: row tiles are whole if that takes no longer than equal parts, which
-    // are joined (or if they are so many that their places would overflow).
+    // are joined (or if they are so many that their places would overflow).  A prompt of 512 tokens takes 28 us in whole row
+    // tiles and 41 in parts, 1024 tokens 42 and 56, chunks of 900 after 1000 209 and 226; two chunks of 512 after 16384 in
+    // whole row tiles 539 and in parts 409.
     __device__ __forceinline__ int64_t measure(const AttentionArgs &a, int workgroups) {
         int64_t items = 0, all = 0;
         float longest = 0.0f, shortest = 3.0e38f;

@@ -3,7 +3,11 @@
 //
 // One wave serves a 32-token tile of one sequence and 64 dimensions of one kv head.
 // Both kernels move each f32 value and each code once and are bound by that and, for
-// a few tokens, by one wave's chain of load, reduction and store.  A tile belongs to
+// a few tokens, by one wave's chain of load, reduction and store.  Three prompts of up to 2048 tokens (62 MB
+// of f32) are appended in 12.6 us, of which some 6 are the quantization's instructions; eight whole sequences
+// of up to 4099 tokens are read back, 165 MB in all, in 29 us while the last-level cache takes the output, and
+// 51 from and to memory (3.2 TB/s; stores that pass the caches by: 45, but 61 instead of 44 for a call by
+// itself, whose output is then not there for its reader).  One token: 4.2 and 3.2 us.  A tile belongs to
 // one wave because two tokens share a byte of the 4-bit value codes: the wave that
 // writes the byte has both tokens, so that no atomics are needed.
 //   keys  : lane = 8 tokens x 8 dimensions: a block's 32 values lie in 4 lanes, whose
