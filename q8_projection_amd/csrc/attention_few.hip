@@ -26,15 +26,18 @@ namespace q8 {
 namespace {
 
 constexpr int kAhead = 8;      // parts whose loads are in flight at once
-constexpr int kMinTiles = 16;  // tiles of a piece of four waves, at least (but for shorter sequences)
+// Tiles of a piece, at least (but for shorter sequences).  One sequence of 500 tokens takes 10.6 us, at 12 11.7; of 4000
+// tokens 14.5, at 24 15.6, at 48 18.4.
+constexpr int kMinTiles = 16;
 constexpr int kPiecesPerSlot = 2;  // pieces for each workgroup that the chip holds (twice as many counters: kCountersPerCu)
 static_assert(2 * 3 * kPiecesPerSlot <= kCountersPerCu);
-constexpr int kBigItems = 4;       // kv heads for a CU, inverse, up to which a workgroup takes a whole CU
+// A workgroup takes a whole CU up to a kv head of some sequence for kBigItems CUs: fewer parts to join.  16 kv heads at 32000 tokens
+// 24.9 us, with workgroups of four waves 33.7, 64 of them 66 and 77; at 2 for kBigItems, 128 of up to 4096 tokens 28.4 and 21.9.
+constexpr int kBigItems = 4;
 
 struct FewArgs {
     AttentionArgs a;
     int pieces;         // wanted
-    int least;          // tiles of a piece, at least (but for shorter sequences)
     uint32_t *arrived;  // [2 pieces], zero between calls
     float *parts;       // [2 pieces][slot]
     int slot;           // floats of a part: rows * (D + 4)
@@ -247,7 +250,7 @@ struct Piece {
 
 // Finds piece after piece, in ascending order.
 struct Pieces {
-    int target;               // tiles of a piece at most
+    int target, slack;        // tiles of a piece, and how many more are no second one
     int s0 = 0;               // sequences s0 .. s0 + 63 are the lanes'
     int64_t pieces = 0, parts = 0;  // before them
     Rows rows;
@@ -262,7 +265,7 @@ struct Pieces {
         return static_cast<uint32_t>(span.n);
     }
     __device__ __forceinline__ void divide() {
-        count = static_cast<uint32_t>((span.n + target - 1) / target);
+        count = span.n ? static_cast<uint32_t>(max((span.n - slack + target - 1) / target, 1)) : 0u;
         scan = wave_scan(count);
         scan_parts = wave_scan(count > 1 ? count : 0u);
     }
@@ -322,7 +325,10 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
     int64_t total = 0;
     for (; pieces.s0 < c.sequences; pieces.s0 += 64) total += lane_of(wave_scan(pieces.look(a, lane)), 63);
     // (no sequence has more than 2^25 tiles)
-    pieces.target = static_cast<int>(min(max((total * c.kv_heads + f.pieces - 1) / f.pieces, int64_t(f.least)), int64_t(1) << 26));
+    // (12 waves take 24 tiles in no more turns than 16, four waves one turn more for every four: one sequence of 517 tokens 10.4 us
+    // with the slack, without it 11.8; drafted tokens of 16 sequences 23.8 with it and 22.0)
+    pieces.slack = WAVES > 4 ? kMinTiles / 2 : 0;
+    pieces.target = static_cast<int>(min(max((total * c.kv_heads + f.pieces - 1) / f.pieces, int64_t(kMinTiles)), int64_t(1) << 26));
     pieces.s0 = 0;
     if (c.sequences > 64) pieces.look(a, lane);
     pieces.divide();
@@ -541,11 +547,9 @@ hipError_t run(FewArgs f, hipStream_t stream) {
     const int cus = device_info().cus;
     if (items * kBigItems <= cus) {
         f.pieces = cus;
-        f.least = kMinTiles * kPerCu;
         few_kernel<BITS, D, NR, 4 * kPerCu><<<dim3(static_cast<uint32_t>(cus + items)), 256 * kPerCu, 0, stream>>>(f);
     } else {
         f.pieces = cus * kPiecesPerSlot * kPerCu;
-        f.least = kMinTiles;
         // every piece a workgroup, unless there are very many
         const int64_t most = std::min<int64_t>(f.pieces + items, 32 * int64_t(f.pieces));
         few_kernel<BITS, D, NR, 4><<<dim3(static_cast<uint32_t>(most)), 256, 0, stream>>>(f);
