@@ -85,7 +85,8 @@ typedef struct {
     const int32_t *starts;  /* [sequences + 1], not decreasing, 4-byte aligned; or NULL: row s is sequence s's
                                (rows == sequences) */
     int64_t rows;           /* rows of the call's arrays, 0 .. 2^20 */
-    int64_t max_rows;       /* rows of one sequence at most, 1 or more (sizes the launches) */
+    int64_t max_rows;       /* rows of one sequence at most, 1 or more (sizes the launches and
+                               chooses the kernels: best not far above the longest) */
 } q8_cache_batch;
 
 /* Bytes of a page (0 for sizes that are refused; pages and data are not looked at). */
