@@ -176,7 +176,8 @@ q8_status q8_attention(const q8_cache *cache, const q8_cache_batch *batch, const
     a.heads = static_cast<int>(heads);
     a.group = a.heads / a.c.kv_heads;
     a.scale = scale;
-    a.window = static_cast<int>(window);
+    // (a window as long as a sequence can be hides nothing; the kernels' at - window, from at >= -kMaxRows on, keeps within 32 bits)
+    a.window = window < kMaxTokens ? static_cast<int>(window) : 0;
     a.out = out;
     a.lse = lse;
     const auto launch = few(a, cache->head_dim) ? q8::launch_few : q8::launch_rows;
