@@ -95,9 +95,10 @@ int64_t q8_cache_page_bytes(const q8_cache *cache);
 /* Write the rows' keys and values into the cache.
  *   k, v : f32 rows of [kv_heads][head_dim], k_ld and v_ld values apart (multiples
  *          of 4 from kv_heads * head_dim to 2^40), 16-byte aligned.
- * Tokens already in the cache stay as they were, those in the same bytes too.  Two
- * rows of one call must not be the same place of a page, nor may calls in flight at
- * once write to one page.  Inputs must be finite.
+ * Tokens already in the cache stay as they were, those in the same bytes too.  Sequences
+ * of one call may have the same pages (chunks of one prompt, say) and write to them, but two
+ * rows must not be the same place of a page; nor may calls in flight at once write to one
+ * page.  Inputs must be finite.
  * Limit: sequences * max_rows * kv_heads * head_dim <= 2^40 (else Q8_E_SHAPE).
  * Errors: Q8_E_NULL, Q8_E_MODE (bits), Q8_E_SHAPE, Q8_E_ALIGN, Q8_E_ALIAS, Q8_E_HIP. */
 q8_status q8_cache_append(const q8_cache *cache, const q8_cache_batch *batch, const float *k, int64_t k_ld,

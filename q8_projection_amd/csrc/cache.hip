@@ -7,9 +7,11 @@
 // of f32) are appended in 12.6 us, of which some 6 are the quantization's instructions; eight whole sequences
 // of up to 4099 tokens are read back, 165 MB in all, in 29 us while the last-level cache takes the output, and
 // 51 from and to memory (3.2 TB/s; stores that pass the caches by: 45, but 61 instead of 44 for a call by
-// itself, whose output is then not there for its reader).  One token: 4.2 and 3.2 us.  A tile belongs to
-// one wave because two tokens share a byte of the 4-bit value codes: the wave that
-// writes the byte has both tokens, so that no atomics are needed.
+// itself, whose output is then not there for its reader).  One token: 4.2 and 3.2 us.  Another
+// sequence of the call may have the same page and the tokens beside a sequence's own (chunks of one prompt that
+// meet there), so a wave writes nothing but its tokens' codes: whole dwords or bytes, and, where a byte of two
+// 4-bit codes may be shared, an exclusive or of what changes (one token 4.1 us and one each of 64 sequences 4.4; with dwords
+// loaded, changed and stored, which loses the other's codes, 3.9 and 4.2; bytes of 8 bits 4.2, so 5.0).
 //   keys  : lane = 8 tokens x 8 dimensions: a block's 32 values lie in 4 lanes, whose
 //           smallest and largest meet in two DPP steps.
 //   values: lane (g, b) = tokens 8 g .. 8 g + 7 of dimensions 4 b .. 4 b + 3: the lane holds
@@ -207,6 +209,19 @@ __device__ __forceinline__ void append(const AppendArgs &a, const Work &w) {
     }
     uint8_t *tile = tile_at<BITS, D>(a.c, w.s, t, w.head);
     if (!tile) return;
+    // 4 bits: the groups of eight tokens that the call has a part of alone (the first and the last can be such), and
+    // what their dwords are, one a lane.  (The bits of this wave's tokens nobody else changes: what they were they are.)
+    const int group[2] = {lo / 8, (hi - 1) / 8};
+    const bool edge[2] = {lo % 8 != 0 || hi < group[0] * 8 + 8, group[1] != group[0] && hi % 8 != 0};
+    const auto edge_at = [&](int i) {
+        return reinterpret_cast<uint32_t *>(tile + T::kValues + (w.part * 4 + group[i]) * 256) + lane;
+    };
+    uint32_t was[2] = {0, 0};
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (edge[i]) was[i] = *edge_at(i);
+    }
 
     // Keys: a pass is 8 tokens.  A block's scale is made by one of its four lanes: lane p of them has pass p's.
     const auto pass_is = [&](int p) { return p * 8 < hi && p * 8 + 8 > lo; };
@@ -273,22 +288,46 @@ __device__ __forceinline__ void append(const AppendArgs &a, const Work &w) {
             else code[e][(n & 3) >> 1] |= q << (16 * (n & 1) + 8 * (n >> 2));
         }
     });
-    // the lane's tokens that are written, and what it keeps of those that are not
+    // the lane's tokens that are written
     const int first = max(lo - g * 8, 0), last = min(hi - g * 8, 8);
-    if (first >= last) return;
-    uint32_t keep[kWords] = {};
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        if (n >= first && n < last) continue;
-        if (BITS == 4) keep[0] |= 0xfu << (4 * n);
-        else keep[(n & 3) >> 1] |= 0xffu << (16 * (n & 1) + 8 * (n >> 2));
-    }
     uint8_t *dst = tile + value_place<BITS, D>(w.part, g, dims);
+    if constexpr (BITS == 4) {
+        if (first == 0 && last == 8)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t *at = reinterpret_cast<uint32_t *>(dst + 16 * e);
+            for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(dst + 16 * e) = code[e][0];
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) at[i] = keep[i] ? (code[e][i] & ~keep[i]) | (at[i] & keep[i]) : code[e][i];
+        for (int i = 0; i < 2; ++i) {
+            if (!edge[i]) continue;
+            // dword 4 c + w of the group is the lane's: from lane 4 w + c / 4 of the group's, its number c % 4
+            const int from = 4 * (16 * group[i] + 4 * (lane & 3) + (lane >> 4));
+            uint32_t mine = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t c = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(code[e][0])));
+                mine = (lane >> 2 & 3) == e ? c : mine;
+            }
+            const int begin = max(lo - group[i] * 8, 0), end = min(hi - group[i] * 8, 8);
+            const uint32_t owned = 0xffffffffu >> (32 - 4 * (end - begin)) << (4 * begin);
+            __hip_atomic_fetch_xor(edge_at(i), (was[i] ^ mine) & owned, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            // tokens 2 i, 2 i + 1, 2 i + 4, 2 i + 5 in the dword's bytes
+            if (first <= 2 * i && last >= 2 * i + 6) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(dst + 16 * e)[i] = code[e][i];
+                continue;
+            }
+            each<4>([&](auto B) {
+                constexpr int byte = B;
+                const int n = 2 * i + byte / 2 + 4 * (byte % 2);
+                if (!token_is(n)) return;
+                if (n >= first && n < last)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[16 * e + 4 * i + byte] = static_cast<uint8_t>(code[e][i] >> (8 * byte));
+            });
+        }
     }
 }
 
