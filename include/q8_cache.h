@@ -116,8 +116,12 @@ q8_status q8_cache_read(const q8_cache *cache, const q8_cache_batch *batch, floa
  *   z_t = scale * sum_j q_j k_tj,  out = sum_t exp(z_t) v_t / sum_t exp(z_t)
  *   lse = ln sum_t exp(z_t)
  *
- * A row that sees no token gives zeros, and -inf.  Sums are held in f32; products
- * are of the cache's exact values with 22 bits or more of q and of exp(z).
+ * A row that sees no token gives zeros, and -inf.  Sums are held in f32; products are of
+ * the cache's exact values with two binary16 words of q and of exp(z):
+ *   scale * q_j is off by 2^-22 of it, or 2^-39 of the largest of its row and head;
+ *   exp(z_t) by 2^-22 of it, or 2^-24 of the largest among the 32 tokens of its tile (2^-36
+ *   in the tile of the row's largest; for weights down to 2^-79 of that one).
+ * scale * log2(e) * q_j and the scores must stay within f32's range.
  *   q     : f32 rows of [heads][head_dim], q_ld values apart (a multiple of 4 from
  *           heads * head_dim to 2^40), 16-byte aligned, finite.
  *   heads : a multiple of kv_heads up to 4096.

@@ -3,8 +3,9 @@
 //
 // Every value of the cache is a binary16 number times a power of two exactly, so one side of
 // each product needs no rounding, and the f32 side is split in two words, x = hi + lo with
-// hi = rne16(x), lo = rne16(x - hi): 22 bits or more of it.  Both words go through the matrix
-// cores into the same f32 sums.
+// hi = rne16(x), lo = rne16(x - hi): 22 bits of it, as long as lo does not end on binary16's grid of
+// 2^-24 (queries are lifted for that, and weights' scale follows the scores).  Both words go through the
+// matrix cores into the same f32 sums.
 //
 // A product's depth may be taken in any order, if both operands take the same, and rows in any: scores are
 // made with keys as rows and queries as columns, sums with the values' dimensions as rows and weights as
@@ -26,11 +27,18 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kNoMax = -3.0e38f;   // the maximum of no scores: weights of masked tokens are then 0, too
-// Weights are exp2(z - m + 11), with m at most 4 below the running maximum: sums are rescaled only where
-// the maximum has grown by more than 4, and a weight's words still end far below it (on binary16's
-// grid of 2^-24, 2^-36 of the largest weight) and never pass 2^15.
-constexpr float kWeightShift = 11.0f, kMaxSlack = 4.0f;
+constexpr float kNoMax = -3.0e38f;   // the scale of no scores: weights of masked tokens are then 0, too
+// Weights are exp2(z - m + 11). m, a whole number (so that rescaling is exact), follows the scores of the tiles that a wave
+// takes one after the other: sums are rescaled only where a row's largest score of a tile is over m + 4.75 or under m - 12, and
+// m becomes that score, rounded down. So a weight never passes 2^15.75 (binary16 ends at 2^16), and the largest of a row and tile
+// is 2^-1 or more, that of the row's largest score 2^11: a weight's words, which end on binary16's grid of 2^-24, are off by 2^-22 of it or by 2^-24 of
+// the largest beside it in its tile. Where one token has nearly all of the weight, m comes down again for the tiles after
+// it (without that, of 2000 tokens 14 nats below such a one the sums were off by 5e-5, plain f32 products' by 4e-7); the
+// tokens of its own tile keep 2^-36 of it.
+constexpr float kWeightShift = 11.0f, kMaxSlack = 4.75f, kMinSlack = 12.0f;
+// What a lane's sum of weights may reach by that, 2^90: with values of 2^16 and the sums of all waves and parts, 2^14
+// together, sums stay below 2^127. So m is at most some 2^79 below a row's largest.
+constexpr float kMaxSum = 90.0f;
 
 __device__ __forceinline__ half2 as_half2(uint32_t v) { return __builtin_bit_cast(half2, v); }
 __device__ __forceinline__ half2 splat(_Float16 v) { return half2{v, v}; }
@@ -132,7 +140,7 @@ __device__ __forceinline__ float2 lane_pair16(float v) {
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // A power of two that brings values of up to `most` into [2^14, 2^15) (small ones below), as its f32
-// exponent field.
+// exponent field.  (Elements under 2^-17 of that have fewer than 22 bits: their second words are off by 2^-39 of it.)
 __device__ __forceinline__ uint32_t lift_of(float most) {
     const int e = static_cast<int>(__builtin_bit_cast(uint32_t, most) >> 23);  // biased
     return static_cast<uint32_t>(min(141 + 127 - e, 253)) << 23;
@@ -228,12 +236,28 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
 }
 
-// Keeps the softmax's maximum at most kMaxSlack below `most`, the lane's largest score, and the sums in step
-// with it: rescale(factor) multiplies the others.
+// Keeps the weights' scale near `most`, the lane's largest score of a tile, and the sums in step with it:
+// rescale(factor) multiplies the others.  (A lane has a part of its row's scores: whether there is anything to do, which
+// is seldom, its column's decide. That is a branch of its own because the sums' registers are moved about in the second.)
 template <typename Max, typename Fn>
 __device__ __forceinline__ void follow_max(float most, float &top, float &sum, Max column_max, Fn rescale) {
-    if (__any(most > top + kMaxSlack)) {
-        const float now = fmaxf(column_max(most), top);
+    constexpr float kMid = 0.5f * (kMaxSlack - kMinSlack), kHalf = 0.5f * (kMaxSlack + kMinSlack);
+    float now = top;
+    bool changes = false;
+    if (__any(fabsf(most - top - kMid) > kHalf)) {
+        const float tile = column_max(most);
+        // (-inf: none of the tile's tokens is seen)
+        const bool under = tile < top - kMinSlack && tile > kNoMax;
+        if (__any(tile > top + kMaxSlack || under)) {
+            now = fmaxf(floorf(tile), top);
+            if (__any(under)) {
+                const float room = floorf(kMaxSum - __builtin_amdgcn_logf(column_max(sum)));
+                now = under ? fmaxf(floorf(tile), top - fminf(fmaxf(room, 0.0f), kMaxSum)) : now;
+            }
+            changes = true;
+        }
+    }
+    if (changes) {
         const float keep = exp2_of(top - now);
         top = now;
         sum *= keep;
@@ -264,8 +288,12 @@ template <int D>
 __device__ __forceinline__ void write_row(const AttentionArgs &a, const Where &at, int dim, f32x4 o, float total, float top) {
     const float f = total > 0 ? 1.0f / total : 0.0f;
     *reinterpret_cast<f32x4 *>(a.out + (at.row * a.heads + at.head) * D + dim) = o * f;
-    if (dim == 0 && a.lse)
-        a.lse[at.row * a.heads + at.head] = total > 0 ? (top - kWeightShift) * kLn2 + logf(total) : -INFINITY;
+    if (dim == 0 && a.lse) {
+        // (the total's exponent joins the scale's, which may be far from it, before they are rounded)
+        const float e = static_cast<float>(__builtin_amdgcn_frexp_expf(total));
+        const float lse = (top + (e - kWeightShift)) * kLn2 + logf(__builtin_amdgcn_frexp_mantf(total));
+        a.lse[at.row * a.heads + at.head] = total > 0 ? lse : -INFINITY;
+    }
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
