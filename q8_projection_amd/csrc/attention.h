@@ -30,14 +30,15 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNoMax = -3.0e38f;   // the scale of no scores: weights of masked tokens are then 0, too
 // Weights are exp2(z - m + 11). m, a whole number (so that rescaling is exact), follows the scores of the tiles that a wave
 // takes one after the other: sums are rescaled only where a row's largest score of a tile is over m + 4.75 or under m - 12, and
-// m becomes that score, rounded down. So a weight never passes 2^15.75 (binary16 ends at 2^16), and the largest of a row and tile
-// is 2^-1 or more, that of the row's largest score 2^11: a weight's words, which end on binary16's grid of 2^-24, are off by 2^-22 of it or by 2^-24 of
-// the largest beside it in its tile. Where one token has nearly all of the weight, m comes down again for the tiles after
-// it (without that, of 2000 tokens 14 nats below such a one the sums were off by 5e-5, plain f32 products' by 4e-7); the
-// tokens of its own tile keep 2^-36 of it.
+// m becomes that score, rounded down. So a weight never passes 2^15.75 (binary16 ends at 2^16), the largest of a row and
+// tile is 2^-1 or more, and that of the row's largest score 2^11: a weight's words, which end on binary16's grid of 2^-24,
+// are off by 2^-22 of it or by 2^-24 of the largest beside it in its tile. Where one token has nearly all of the weight,
+// m comes down again for the tiles after it; the tokens of its own tile keep 2^-36 of it. (The last rows of a prompt of
+// 4096 tokens whose first has a value of zero and scores 14 nats above the others, 128 dimensions: off by 8e-7 in the
+// 2-norm, by 3e-6 where m only goes up; 16 nats above, 5e-6 and 2e-5.)
 constexpr float kWeightShift = 11.0f, kMaxSlack = 4.75f, kMinSlack = 12.0f;
-// What a lane's sum of weights may reach by that, 2^90: with values of 2^16 and the sums of all waves and parts, 2^14
-// together, sums stay below 2^127. So m is at most some 2^79 below a row's largest.
+// What a lane's sum of weights may reach when m comes down, 2^90 (so m is at most some 2^79 below a row's largest): with
+// four lanes, values of 2^16, 12 waves and 3072 parts sums stay below 2^125.
 constexpr float kMaxSum = 90.0f;
 
 __device__ __forceinline__ half2 as_half2(uint32_t v) { return __builtin_bit_cast(half2, v); }

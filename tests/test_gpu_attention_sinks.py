@@ -3,10 +3,10 @@ below the largest one.
 
 Bound of the outputs.  A weight w_t goes to the matrix cores in two binary16 words of w_t / m, where the power of two m
 follows the tiles of 32 tokens that a wave takes one after the other: the largest weight that a row has in a tile is
-2^-1 or more of m's scale (a tile that is 12 powers of two below 2^11 lowers m, down to 2^-79 of a row's largest weight: 54 nats), and in the tile of the row's largest weight
-2^11 or more.  The words are off by 2^-22 w_t (half a step of 11 bits, twice) or, where the second ends on binary16's grid
-of 2^-24, by 2^-25: 2^-24 of the largest weight of the tile, 2^-36 in the tile of the row's largest.  With everything else as in
-cache_reference.py,
+2^-1 or more of m's scale (a tile that is 12 powers of two below 2^11 lowers m, down to 2^-79 of a row's largest
+weight: 54 nats), and in the tile of the row's largest weight 2^11 or more.  The words are off by 2^-22 w_t (half a step of
+11 bits, twice) or, where the second ends on binary16's grid of 2^-24, by 2^-25: 2^-24 of the largest weight of the
+tile, 2^-36 in the tile of the row's largest.  With everything else as in cache_reference.py,
 
     |out - ref| <= A (2 ez + 2^-20 + (T / 8 + 64) 2^-24) + sum_t e_t |v_t| / sum_t exp(z_t),
     e_t = 2^-24 max over t's tile of exp(z) (2^-36 of it in the tile of the largest z)
@@ -119,3 +119,22 @@ def test_heavy_tokens_of_many_weights(bits, dim, new):
         p = Pool(bits, 2, dim, 64, lens, seed=dim)
         p.k, p.v = map(list, zip(*(sinks(rng, n, dim, 2, heavy, order) for n in lens)))
         check(p.fill(), lens, [new] * 12, 4, rng)
+
+
+@pytest.mark.parametrize("bits,dim", [(4, 64), (4, 128), (8, 256)])
+@pytest.mark.parametrize("new", [1, 40])
+def test_heavy_tokens_beside_values_as_large_as_there_are(bits, dim, new):
+    """A heavy token in every third tile: every wave's sums are lifted as far as they are, many parts of them joined."""
+    say("heavy, large values", bits, dim, new)
+    rng = np.random.default_rng(new)
+    n, p = 9000, Pool(bits, 1, dim, 64, [9000], seed=dim)
+    for above in (45, 70):  # (70: weights of 2^-101 of the largest, under what the words hold; the sums have to hold up)
+        k, v = sinks(rng, n, dim, 1, list(range(7, n, 96)), [above] * 94)
+        p.k, p.v = [k], [v * np.float32(4e4)]
+        p.fill()
+        if above == 45:
+            check(p, [n], [new], 4, rng)
+        q = torch.full((new, 4, dim), 0.25, device="cuda")
+        q[..., 0] = 8
+        out, lse = q8.attention(p.cache, p.batch(starts=[0, new], rows=new), q)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all() and (out >= 0).all()
