@@ -52,7 +52,8 @@ __device__ __forceinline__ float span_of(float low, float high) {
 template <int BITS>
 __device__ __forceinline__ float scale_of(float span) {
     using F = Format<BITS>;
-    const float t = fminf(span / F::kSteps, F::kTop);
+    // (a quotient that rounds to 0 is one of a span over 0)
+    const float t = fminf(fmaxf(span / F::kSteps, fminf(span, 0x1p-149f)), F::kTop);
     constexpr uint32_t step = (1u << F::kDrop) - 1;
     const float up = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, t) + step) & ~step);
     const float low = ceilf(t * (1.0f / F::kLowest)) * F::kLowest;  // binary16's subnormal grid
