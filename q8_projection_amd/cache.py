@@ -95,7 +95,7 @@ class CacheBatch:
         self._bytes = {}
 
     def _workspace_bytes(self, cache, heads: int) -> int:
-        key = (cache.kv_heads, cache.head_dim, cache.bits, heads)
+        key = (cache.kv_heads, cache.head_dim, cache.page_tokens, cache.bits, heads)
         if key not in self._bytes:
             with torch.cuda.device(self.device):
                 self._bytes[key] = int(_q8.lib().q8_attention_workspace_bytes(cache._ref, self._ref, heads))
