@@ -325,9 +325,11 @@ __global__ __launch_bounds__(64 * WAVES, (kWavesPerSimd<BITS, D, NR>)) void few_
     int64_t total = 0;
     for (; pieces.s0 < c.sequences; pieces.s0 += 64) total += lane_of(wave_scan(pieces.look(a, lane)), 63);
     // (no sequence has more than 2^25 tiles)
-    // (12 waves take 24 tiles in no more turns than 16, four waves one turn more for every four: one sequence of 517 tokens 10.4 us
-    // with the slack, without it 11.8; drafted tokens of 16 sequences 23.8 with it and 22.0)
-    pieces.slack = WAVES > 4 ? kMinTiles / 2 : 0;
+    // A large workgroup takes up to half more than a least piece in a turn more at most, and has no parts to join then: 517 tokens
+    // (12 waves) 10.4 us with the slack, without it 11.8; 700 tokens (8 waves, up to 128 dimensions) 10.7 to 15.1, without
+    // it 11.0 to 15.4. 256 dimensions pay more for the turn: 700 tokens 16.2 (4 bits) and 22.0 (8 bits) with it, 13.9 and 18.4
+    // without it. Four waves take a turn more for every four tiles: drafted tokens of 16 sequences 23.8 with it and 22.0.
+    pieces.slack = WAVES > 4 && D < 256 ? kMinTiles / 2 : 0;
     pieces.target = static_cast<int>(min(max((total * c.kv_heads + f.pieces - 1) / f.pieces, int64_t(kMinTiles)), int64_t(1) << 26));
     pieces.s0 = 0;
     if (c.sequences > 64) pieces.look(a, lane);
