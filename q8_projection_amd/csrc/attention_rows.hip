@@ -19,8 +19,8 @@
 // sequence, of which every workgroup takes an equal part, and a row tile that several share is joined by the last
 // of them, in the order of the workgroups.  What is estimated to take longer is not taken (Line::measure).
 //
-// Measured: a prompt of 2048 tokens, 32 heads of 8 kv heads and 128 dimensions, 4 bits: 89 us for 34 GFLOP, 0.78 PFLOP/s of
-// binary16 products with both words (a large library product reaches 1.1); two chunks of 512 tokens after 16384: 384 us for 196
+// Measured: a prompt of 2048 tokens, 32 heads of 8 kv heads and 128 dimensions, 4 bits: 88 us for 34 GFLOP, 0.78 PFLOP/s of
+// binary16 products with both words (a large library product reaches 1.1); two chunks of 512 tokens after 16384: 383 us for 196
 // GFLOP, 1.02 PFLOP/s.  A stage takes some 3500 cycles of 1.9 GHz, 2048 of which the matrix cores work; the rest is the issue
 // port, which a product takes for half of its time and each weight (an exponential, two words) and code for its own.
 // Beside the stages a row tile takes some 12 us: its queries, the first tiles' way through memory, the output.
@@ -71,7 +71,13 @@ __device__ __forceinline__ Rows rows_of_tile(const AttentionArgs &a, const Rows 
 // it sees, in sixteenths: these grow evenly from the sequence's first row tile to its last.
 constexpr int kLinePart = 16;
 // What a row tile costs besides its tiles (queries, first tiles and ends of the pipeline, the output), in tiles of
-// tokens; a part that does not end there costs as much and a join.
+// tokens; a part that does not end there costs as much and a join.  It decides between whole row tiles and parts. us here, and
+// at half and (64 and 256 dimensions) one and a half times or (128) twice as much:
+//   64 dimensions:  8 heads of 4 kv heads, prompt of 512 tokens 19.1, 27.0, 19.0; of 2048 37.0, 35.1, 44.9;
+//                   32 of 8, chunks of 700 in a window of 1024, 8 bits 76.7, 74.7, 85.9
+//   128 dimensions: 32 of 8, prompt of 512 26.9, 47.7, 26.9; of 1024 40.4, 55.7, 40.5; 8 of 4, of 512 38.0, 36.7, 26.1;
+//                   8 of 4, 100 rows after 4000 tokens 43.2, 43.2, 44.6
+//   256 dimensions: 8 of 4, prompt of 512 35.1, 47.0, 35.1; the chunks in a window 84.6, 94.5, 94.4
 constexpr int cost_of(int d) { return d == 64 ? 24 : d == 128 ? 12 : 18; }
 template <int D>
 struct Line {

@@ -3,11 +3,11 @@
 //
 // One wave serves a 32-token tile of one sequence and 64 dimensions of one kv head.
 // Both kernels move each f32 value and each code once and are bound by that and, for
-// a few tokens, by one wave's chain of load, reduction and store.  Three prompts of up to 2048 tokens (62 MB
-// of f32) are appended in 12.6 us, of which some 6 are the quantization's instructions; eight whole sequences
+// a few tokens, by one wave's chain of load, reduction and store.  Three prompts of up to 2048 tokens (31 MB
+// of f32, 4.4 MB of codes) are appended in 11.9 us, of which some 6 are the quantization's instructions; eight whole sequences
 // of up to 4099 tokens are read back, 165 MB in all, in 29 us while the last-level cache takes the output, and
 // 51 from and to memory (3.2 TB/s; stores that pass the caches by: 45, but 61 instead of 44 for a call by
-// itself, whose output is then not there for its reader).  One token: 4.2 and 3.2 us.  Another
+// itself, whose output is then not there for its reader).  One token is read in 3.2 us.  Another
 // sequence of the call may have the same page and the tokens beside a sequence's own (chunks of one prompt that
 // meet there), so a wave writes nothing but its tokens' codes: whole dwords or bytes, and, where a byte of two
 // 4-bit codes may be shared, an exclusive or of what changes (one token 4.1 us and one each of 64 sequences 4.4; with dwords
