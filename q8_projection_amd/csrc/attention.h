@@ -38,7 +38,7 @@ constexpr float kNoMax = -3.0e38f;   // the scale of no scores: weights of maske
 // 2-norm, by 3e-6 where m only goes up; 16 nats above, 5e-6 and 2e-5.)
 constexpr float kWeightShift = 11.0f, kMaxSlack = 4.75f, kMinSlack = 12.0f;
 // What a lane's sum of weights may reach when m comes down, 2^90 (so m is at most some 2^79 below a row's largest): with
-// four lanes, values of 2^16, 12 waves and 3072 parts sums stay below 2^125.
+// four lanes, values of 2^16, 12 waves and 2^12 parts sums stay below 2^125.
 constexpr float kMaxSum = 90.0f;
 
 __device__ __forceinline__ half2 as_half2(uint32_t v) { return __builtin_bit_cast(half2, v); }
